@@ -239,6 +239,95 @@ size_t moe_workspace_bytes(const moe_layer *layer, int32_t T_max);
 moe_status moe_stack_forward(const moe_layer *layers, int32_t n_layers, void *x_inout, int32_t T,
                              float *y_last_opt, void *ws, size_t ws_bytes, void *stream);
 
+/* A dense projection with packed weights: one matrix [rows][cols] in the
+ * experts' formats (the projections around the routed layer and the output
+ * head; the pages quantise the whole model, page 1 "Quantization Configuration
+ * Example"). */
+typedef struct moe_linear {
+  int32_t rows;      /* outputs N, 1 .. 2^24                                    */
+  int32_t cols;      /* inputs, a multiple of 32, <= 65536                      */
+  int32_t qfmt;      /* moe_qfmt                                                */
+  int32_t act;       /* moe_act: type of x                                      */
+  int32_t out;       /* moe_act: type of y                                      */
+  moe_qmat w;        /* codes [rows][cols*bits/8], scales (mins) [rows][cols/32] */
+  const float *bias; /* [rows] fp32 added to the sums, or NULL                  */
+} moe_linear;
+
+/* y[t][n] = round_out( sum_k w[n][k] x[t][k] + bias[n] ),  t < T, n < rows
+ * with fp32 sums and one rounding at the end.  Row t of x starts at
+ * x + t * x_stride elements, row t of y at y + t * y_stride (x_stride >= cols,
+ * y_stride >= rows; not read when T == 1).  Every row of x starts at a multiple
+ * of 16 bytes, y is aligned to its element.  Elements of y between rows and
+ * y_stride are not written.  x and y do not overlap.  A NaN or infinity in row
+ * t of x gives NaN or infinity in row t of y and nowhere else; finite values
+ * beyond 2^120 may overflow.  T <= 2^20.  No workspace. */
+moe_status moe_linear_q(const moe_linear *lin, const void *x, int64_t x_stride, int32_t T,
+                        void *y, int64_t y_stride, void *stream);
+
+/* One step of a beam search: batch sequences of `beams` hypotheses each. */
+typedef struct moe_beam {
+  int32_t batch;  /* sequences B, >= 0                                          */
+  int32_t beams;  /* hypotheses per sequence W, 1..64                           */
+  int32_t vocab;  /* V, 1 .. 2^24                                               */
+  int32_t n_out;  /* candidates returned per sequence, 1..128                   */
+  int32_t act;    /* moe_act: type of the logits                                */
+  int32_t eos;    /* token a finished beam is carried on with, or -1            */
+} moe_beam;
+
+/* Selection over beams and vocabulary.  Row r = b W + w of the logits (at
+ * logits + r * logits_stride elements, logits_stride >= V) belongs to beam w of
+ * sequence b, which has the log-probability scores[b][w] so far.
+ *   A_r         = the allowed tokens: all, or those whose bit is set in
+ *                 allowed_opt (bit v mod 32 of word v div 32 at
+ *                 allowed_opt + r * allowed_stride words; allowed_stride 0:
+ *                 one mask for every row).  Logits outside A_r count as -inf
+ *                 whatever is stored there, NaN included.
+ *   L_r         = log sum_{v in A_r} exp(logits[r][v])
+ *   total(w, v) = scores[b][w] + (logits[r][v] - L_r)          (in 64 bits)
+ * A beam with finished_opt[b][w] != 0 has the one candidate (w, eos) with
+ * total scores[b][w]; its logits are not read.  A row whose score or L_r is not
+ * finite (nothing allowed, a NaN or +inf among the allowed logits, a score of
+ * -inf) has no candidates, and a logit of -inf is none.
+ * out_parent / out_token / out_score [B][n_out] receive the n_out candidates of
+ * the largest total, in descending order, equal totals by the lower w V + v
+ * (within a beam the order is that of the logits); out_score is the total
+ * rounded to fp32.  Where there are fewer candidates the rest are
+ * (-1, -1, -inf).  Results do not depend on the launch or on other rows.
+ * Workspace: at least moe_beam_workspace_bytes(beam), 256-byte aligned. */
+moe_status moe_beam_select(const moe_beam *beam, const void *logits, int64_t logits_stride, const float *scores,
+                           const uint8_t *finished_opt, const uint32_t *allowed_opt, int64_t allowed_stride,
+                           float *out_score, int32_t *out_parent, int32_t *out_token,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_beam_select needs (host-only; 0 for an invalid
+ * descriptor, 256 for batch == 0). */
+size_t moe_beam_workspace_bytes(const moe_beam *beam);
+
+/* One state tensor of the beams: row r = b W + w holds `chunks` pieces of
+ * chunk_bytes contiguous bytes, piece c of row r at
+ * base + r * row_stride + c * chunk_stride (strides in bytes; a row stride is
+ * not read for one row, a chunk stride not for one piece). */
+typedef struct moe_state {
+  const void *src;
+  void *dst;
+  int64_t chunk_bytes;
+  int64_t chunks;
+  int64_t src_row_stride, src_chunk_stride;
+  int64_t dst_row_stride, dst_chunk_stride;
+} moe_state;
+
+/* The beams' states follow their parents, for every state of the HOST array
+ * `states`:
+ *   dst row b W + i  =  src row b W + parent[b * parent_stride + i],  i < W
+ * A parent outside [0, W) leaves its row of dst as it is.  dst may be src
+ * itself with the same strides (in place: rows that are their own parent are
+ * not touched); otherwise their byte ranges must not overlap.  The pieces of
+ * one dst do not overlap each other, and no two states share written bytes.
+ * parent_stride >= W (not read for one sequence): out_parent of
+ * moe_beam_select with n_out >= W fits.  beams 1..64.  No workspace. */
+moe_status moe_beam_reorder(const moe_state *states, int32_t n_states, const int32_t *parent, int64_t parent_stride,
+                            int32_t batch, int32_t beams, void *stream);
+
 /* Test hook: dequantise rows x cols of one packed matrix (expert 0 of `m`)
  * into out [rows][cols] fp32, with the format's definition (Q4: s*(u-8);
  * Q2: fmaf(s, u, m), one rounding). */

@@ -28,8 +28,8 @@ ACT = {"f32": MOE_ACT_F32, "bf16": MOE_ACT_BF16}
 
 EXPORTS = ("moe_router_topk", "moe_permute", "moe_expert_ffn_q", "moe_expert_gate_up_q", "moe_expert_down_q",
            "moe_combine", "moe_layer_forward", "moe_layer_forward_noalloc",
-           "moe_workspace_bytes", "moe_stack_forward", "moe_dequant", "moe_status_str", "moe_abi_version",
-           "moe_range_checks")
+           "moe_workspace_bytes", "moe_stack_forward", "moe_linear_q", "moe_beam_select", "moe_beam_workspace_bytes",
+           "moe_beam_reorder", "moe_dequant", "moe_status_str", "moe_abi_version", "moe_range_checks")
 
 
 class MoeError(RuntimeError):
@@ -51,6 +51,22 @@ class c_layer(ctypes.Structure):
                 ("top_k", ctypes.c_int32), ("qfmt", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("router_w", ctypes.c_void_p), ("router_b", ctypes.c_void_p),
                 ("routed", c_experts), ("shared", c_experts), ("hot_experts", ctypes.c_int32)]
+
+
+class c_linear(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("qfmt", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("out", ctypes.c_int32), ("w", c_qmat), ("bias", ctypes.c_void_p)]
+
+
+class c_beam(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("beams", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("n_out", ctypes.c_int32), ("act", ctypes.c_int32), ("eos", ctypes.c_int32)]
+
+
+class c_state(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("chunk_bytes", ctypes.c_int64),
+                ("chunks", ctypes.c_int64), ("src_row_stride", ctypes.c_int64), ("src_chunk_stride", ctypes.c_int64),
+                ("dst_row_stride", ctypes.c_int64), ("dst_chunk_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -77,6 +93,10 @@ def lib() -> ctypes.CDLL:
             "moe_layer_forward_noalloc": [lp, vp, i32, vp, vp, vp, vp, vp],
             "moe_stack_forward": [lp, i32, vp, i32, vp, vp, sz, vp],
             "moe_dequant": [ctypes.POINTER(c_qmat), i32, i32, i32, vp, vp],
+            "moe_linear_q": [ctypes.POINTER(c_linear), vp, ctypes.c_int64, i32, vp, ctypes.c_int64, vp],
+            "moe_beam_select": [ctypes.POINTER(c_beam), vp, ctypes.c_int64, vp, vp, vp, ctypes.c_int64, vp, vp, vp, vp,
+                                sz, vp],
+            "moe_beam_reorder": [ctypes.POINTER(c_state), i32, vp, ctypes.c_int64, i32, i32, vp],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -84,6 +104,8 @@ def lib() -> ctypes.CDLL:
             fn.restype = ctypes.c_int
         L.moe_workspace_bytes.argtypes = [lp, i32]
         L.moe_workspace_bytes.restype = sz
+        L.moe_beam_workspace_bytes.argtypes = [ctypes.POINTER(c_beam)]
+        L.moe_beam_workspace_bytes.restype = sz
         L.moe_status_str.argtypes = [ctypes.c_int]
         L.moe_status_str.restype = ctypes.c_char_p
         L.moe_abi_version.argtypes = []
@@ -410,6 +432,257 @@ def moe_dequant(codes, scales, mins, qfmt, rows, cols, out, stream=None):
     m = c_qmat(_ptr(codes, device=dev), _ptr(scales, device=dev), _ptr(mins, device=dev))
     _check("moe_dequant", lib().moe_dequant(ctypes.byref(m), q, int(rows), int(cols), _ptr(out, torch.float32),
                                             _stream(stream)))
+
+
+# ------------------------------------------------------------------ around the layer
+
+def _need_rows(name: str, t: torch.Tensor, rows: int, cols: int, dtype):
+    """Type, dtype and shape of a matrix of at least ``rows`` rows of ``cols``
+    elements, each row contiguous (the row stride is the caller's)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [>={rows}][{cols}], got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)}, {cols} columns)")
+
+
+def _addr(name: str, t: torch.Tensor, device) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor must live in device memory")
+    if t.device != device:
+        raise ValueError(f"{name}: tensor on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+class _DeviceBound(Bound):
+    """A Bound call that makes its tensors' device current for the launch."""
+
+    def __init__(self, name: str, args: tuple, keep: tuple, device: torch.device):
+        super().__init__(name, args, keep)
+        self.device = device
+
+    def __call__(self):
+        if torch.cuda.current_device() == self.device.index:
+            st = self.fn(*self.args)
+        else:
+            with torch.cuda.device(self.device):
+                st = self.fn(*self.args)
+        if st != MOE_OK:
+            _check(self.name, st)
+
+
+def _stream_on(stream, device) -> Optional[int]:
+    """The given stream, or the current one of the tensors' device."""
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+
+
+class Linear:
+    """A moe_linear descriptor over device tensors (kept alive by this object):
+    a matrix [rows][cols] in one of the packed formats.
+
+    codes uint8 [rows][cols*bits/8]; scales and mins (2-bit format only) 16-bit
+    planes [rows][cols/32]; bias fp32 [rows] or None.  ``act`` is the type of x,
+    ``out`` that of y ("f32" or "bf16").  A one-matrix expert set ([1][rows][..])
+    is taken as it is."""
+
+    def __init__(self, *, rows: int, cols: int, qfmt, act, codes: torch.Tensor, scales: torch.Tensor,
+                 mins: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, out="f32"):
+        self.qfmt, self.act, self.out = QFMT.get(qfmt, qfmt), ACT.get(act, act), ACT.get(out, out)
+        if self.qfmt not in CODE_BITS:
+            raise ValueError(f"unknown format {qfmt!r}")
+        for name, a in (("act", self.act), ("out", self.out)):
+            if a not in (MOE_ACT_F32, MOE_ACT_BF16):
+                raise ValueError(f"{name} must be 'f32' or 'bf16'")
+        self.rows, self.cols = int(rows), int(cols)
+        self.act_dtype, self.out_dtype = _act_dtype(self.act), _act_dtype(self.out)
+        nb = self.cols * CODE_BITS[self.qfmt] // 8
+        if codes.dtype != torch.uint8 or tuple(codes.shape) not in ((self.rows, nb), (1, self.rows, nb)):
+            raise ValueError(f"codes must be uint8 [{self.rows}][{nb}], got {codes.dtype} {tuple(codes.shape)}")
+        if (mins is None) != (self.qfmt != MOE_Q2_ASYM_G32):
+            raise ValueError("mins are required for the 2-bit format only")
+        ng = self.cols // 32
+        for name, t in (("scales", scales), ("mins", mins)):
+            if t is not None and (t.element_size() != 2 or tuple(t.shape) not in ((self.rows, ng), (1, self.rows, ng))):
+                raise ValueError(f"{name} must be 16-bit [{self.rows}][{ng}]")
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (self.rows,)):
+            raise ValueError(f"bias must be fp32 [{self.rows}]")
+        self.device = codes.device
+        self._keep = (codes, scales, mins, bias)
+        dev = self.device
+        self.c = c_linear(self.rows, self.cols, self.qfmt, self.act, self.out,
+                          c_qmat(_ptr(codes, device=dev), _ptr(scales, device=dev), _ptr(mins, device=dev)),
+                          _ptr(bias, device=dev))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def _linear_args(lin: Linear, x, T, y, stream):
+    T = int(T)
+    _need_rows("x", x, T, lin.cols, lin.act_dtype)
+    _need_rows("y", y, T, lin.rows, lin.out_dtype)
+    return (lin.ref, _addr("x", x, lin.device), x.stride(0) if T > 1 else lin.cols, T, _addr("y", y, lin.device),
+            y.stride(0) if T > 1 else lin.rows, _stream_on(stream, lin.device))
+
+
+def bind_linear_q(lin: Linear, x, T, y, stream=None) -> Bound:
+    """moe_linear_q(...) as a Bound call."""
+    return _DeviceBound("moe_linear_q", _linear_args(lin, x, T, y, stream), (lin, x, y, stream), lin.device)
+
+
+def moe_linear_q(lin: Linear, x, T, y, stream=None):
+    """y[:T] = x[:T] W^T + bias.  x [>=T][cols] and y [>=T][rows] may have any
+    row stride (x: rows at multiples of 16 bytes)."""
+    bind_linear_q(lin, x, T, y, stream)()
+
+
+class Beam:
+    """A moe_beam descriptor: the shape of one beam search's step.  ``act`` is
+    the type of the logits, ``eos`` the token finished beams are carried on with."""
+
+    def __init__(self, *, batch: int, beams: int, vocab: int, n_out: int, act="f32", eos: int = -1):
+        self.batch, self.beams, self.vocab, self.n_out, self.eos = int(batch), int(beams), int(vocab), int(n_out), int(eos)
+        self.act = ACT.get(act, act)
+        self.c = c_beam(self.batch, self.beams, self.vocab, self.n_out, self.act, self.eos)
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def moe_beam_workspace_bytes(beam: Beam) -> int:
+    return int(lib().moe_beam_workspace_bytes(beam.ref))
+
+
+def beam_workspace(beam: Beam, device=None) -> torch.Tensor:
+    """A device workspace tensor of moe_beam_workspace_bytes(beam) bytes."""
+    n = moe_beam_workspace_bytes(beam)
+    if n == 0:
+        raise MoeError("moe_beam_workspace_bytes", MOE_E_ARG, "invalid beam descriptor")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _beam_args(beam: Beam, logits, scores, out_score, out_parent, out_token, finished, allowed, ws, stream):
+    rows, n = beam.batch * beam.beams, beam.batch * beam.n_out
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError(f"logits: expected a torch.Tensor, got {type(logits).__name__}")
+    dev = logits.device
+    _need("scores", scores, rows, torch.float32)
+    _need("out_score", out_score, n, torch.float32)
+    _need("out_parent", out_parent, n, torch.int32)
+    _need("out_token", out_token, n, torch.int32)
+    _need("finished", finished, rows, torch.uint8)
+    ld_allowed = 0
+    if allowed is not None:
+        words = (beam.vocab + 31) // 32
+        if allowed.dim() != 2 or allowed.shape[0] not in (1, rows) or allowed.shape[1] != words:
+            raise ValueError(f"allowed must be int32 [1 or {rows}][{words}], got {tuple(allowed.shape)}")
+        ld_allowed = allowed.stride(0) if allowed.shape[0] > 1 else 0
+        _need_rows("allowed", allowed, allowed.shape[0], words, torch.int32)
+    _need_rows("logits", logits, rows, beam.vocab, _act_dtype(beam.act))
+    lp = _addr("logits", logits, dev)
+    ap = None if allowed is None else _addr("allowed", allowed, dev)
+    w, wn = (None, 0) if ws is None else (_ptr(ws, torch.uint8, dev), ws.numel())
+    return (beam.ref, lp, logits.stride(0) if rows > 1 else beam.vocab, _ptr(scores, None, dev), _ptr(finished, None, dev),
+            ap, ld_allowed, _ptr(out_score, None, dev), _ptr(out_parent, None, dev), _ptr(out_token, None, dev), w, wn,
+            _stream_on(stream, dev))
+
+
+def bind_beam_select(beam: Beam, logits, scores, out_score, out_parent, out_token, finished=None, allowed=None, ws=None,
+                     stream=None) -> Bound:
+    """moe_beam_select(...) as a Bound call."""
+    return _DeviceBound("moe_beam_select",
+                        _beam_args(beam, logits, scores, out_score, out_parent, out_token, finished, allowed, ws, stream),
+                        (beam, logits, scores, out_score, out_parent, out_token, finished, allowed, ws, stream),
+                        logits.device)
+
+
+def moe_beam_select(beam: Beam, logits, scores, out_score, out_parent, out_token, finished=None, allowed=None, ws=None,
+                    stream=None):
+    """The n_out best continuations of each sequence.  logits [batch*beams][vocab]
+    (any row stride), scores [batch][beams]; finished uint8 [batch][beams];
+    allowed int32 bit masks [1 or batch*beams][(vocab+31)//32]."""
+    bind_beam_select(beam, logits, scores, out_score, out_parent, out_token, finished, allowed, ws, stream)()
+
+
+def _pieces(t: torch.Tensor):
+    """(contiguous elements, count, element stride) of a row of a state tensor:
+    one row is ``count`` equally spaced runs of contiguous elements."""
+    dims = [(n, s) for n, s in zip(t.shape[1:], t.stride()[1:]) if n != 1]
+    run = 1
+    while dims and dims[-1][1] == run:
+        run *= dims.pop()[0]
+    if not dims:
+        return run, 1, 0
+    count, stride = dims[-1]
+    for n, s in reversed(dims[:-1]):
+        if s != stride * count:
+            raise ValueError("state: a row must be equally spaced contiguous pieces")
+        count *= n
+    return run, count, stride
+
+
+def _state(src: torch.Tensor, dst: torch.Tensor, rows: int, device) -> c_state:
+    for name, t in (("state", src), ("dst", dst)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if t.dim() < 1 or t.shape[0] != rows:
+            raise ValueError(f"{name} must have {rows} rows (batch * beams), got {tuple(t.shape)}")
+    if src.shape != dst.shape or src.dtype != dst.dtype:
+        raise ValueError("a state and its dst must have the same shape and type")
+    if src.numel() == 0:
+        return c_state()
+    (r0, n0, s0), (r1, n1, s1) = _pieces(src), _pieces(dst)
+    run = min(r0, r1)
+    if r0 > run:  # a contiguous row next to one in pieces
+        if n0 != 1:
+            raise ValueError("state: the pieces of a state and its dst must match")
+        n0, s0 = r0 // run, run
+    if r1 > run:
+        if n1 != 1:
+            raise ValueError("state: the pieces of a state and its dst must match")
+        n1, s1 = r1 // run, run
+    if n0 != n1:
+        raise ValueError("state: the pieces of a state and its dst must match")
+    for t in (src, dst):
+        if not t.is_cuda:
+            raise ValueError("state: tensor must live in device memory")
+        if t.device != device:
+            raise ValueError(f"state: tensor on {t.device}, expected {device}")
+    e = src.element_size()
+    return c_state(src.data_ptr(), dst.data_ptr(), run * e, n0, src.stride(0) * e, s0 * e, dst.stride(0) * e, s1 * e)
+
+
+def bind_beam_reorder(states, parent, batch: int, beams: int, dst=None, stream=None) -> Bound:
+    """moe_beam_reorder(...) as a Bound call."""
+    states = list(states)
+    dst = states if dst is None else list(dst)
+    if len(dst) != len(states):
+        raise ValueError(f"{len(states)} states, {len(dst)} destinations")
+    rows = int(batch) * int(beams)
+    dev = parent.device
+    if parent.dtype != torch.int32 or parent.dim() != 2 or parent.shape[0] < batch or parent.shape[1] < beams:
+        raise ValueError(f"parent must be int32 [>={batch}][>={beams}], got {parent.dtype} {tuple(parent.shape)}")
+    _need_rows("parent", parent, int(batch), parent.shape[1], torch.int32)
+    arr = (c_state * len(states))(*[_state(s, d, rows, dev) for s, d in zip(states, dst)])
+    pp = _addr("parent", parent, dev)
+    return _DeviceBound("moe_beam_reorder", (arr, len(states), pp, parent.stride(0) if batch > 1 else int(beams),
+                                             int(batch), int(beams), _stream_on(stream, dev)),
+                        (states, dst, parent, stream), dev)
+
+
+def moe_beam_reorder(states, parent, batch: int, beams: int, dst=None, stream=None):
+    """Every state's row b * beams + i becomes its row b * beams + parent[b][i],
+    in place or written to ``dst``.  states: tensors [batch*beams][...] whose
+    rows are contiguous or equally spaced contiguous pieces (a cache's filled
+    part, cache[:, :, :length], is); parent int32 [batch][>= beams]."""
+    bind_beam_reorder(states, parent, batch, beams, dst, stream)()
 
 
 def moe_abi_version() -> int:

@@ -157,6 +157,39 @@ hipError_t launch_fused_gateup(const RouterArgs& r, const PermuteArgs& pm, const
 bool fused_down1_ok(int T, int K, int E, int I);
 hipError_t launch_fused_down1(const FfnArgs& a, const CombineArgs& c, hipStream_t s);
 
+// ---------------------------------------------------------------- dense projection
+struct LinearArgs {
+  const uint8_t* codes;    // [N][K*bits/8]
+  const uint16_t* scales;  // [N][K/32]
+  const uint16_t* mins;    // [N][K/32] (2-bit) or null
+  const float* bias;       // [N] or null
+  const void* x;           // [T][ldx] act
+  void* y;                 // [T][ldy] out
+  int64_t ldx, ldy;        // elements
+  int T, N, K, qfmt, act, out;
+};
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- beam search
+struct BeamArgs {
+  const void* logits;        // [B*W][ld] act
+  int64_t ld;                // elements
+  const float* scores;       // [B][W]
+  const uint8_t* finished;   // [B][W] or null
+  const uint32_t* allowed;   // [B*W][ld_allowed] or null
+  int64_t ld_allowed;        // words, 0: one mask for every row
+  float* out_score;          // [B][n]
+  int32_t* out_parent;       // [B][n]
+  int32_t* out_token;        // [B][n]
+  void* ws;
+  int B, W, V, n, act, eos;
+};
+size_t beam_ws_bytes(int B, int W, int V, int n, int act);
+hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
+// states: host array of n descriptors that passed the entry point's checks
+hipError_t launch_beam_reorder(const moe_state* states, int n, const int32_t* parent, int64_t ldp, int B, int W,
+                               hipStream_t s);
+
 // ---------------------------------------------------------------- test hook
 hipError_t launch_dequant(const QMat& m, int qfmt, int rows, int cols, float* out, hipStream_t s);
 
