@@ -1,43 +1,33 @@
-// Dense projection with packed group-32 weights, y = x W^T + bias, on the matrix
-// cores (fragments and arithmetic: linear_frag.h).
+// Dense projection with packed group-32 weights, y = x W^T + bias (fragments and
+// arithmetic: linear_frag.h).  Five kernels by the number of tokens T, all with
+// the weights' loads past the caches and whole cache lines per row:
 //
-// Few tokens read every weight once and do little with it, so both kernels keep
-// the weights out of LDS: a lane loads the whole group (16, 12 or 8 bytes) that
-// it unpacks, 16 output rows x 4 groups a wave and load.
+// k_linear_one (T = 1).  A lane is a group: it unpacks 32 codes and multiplies
+// them with its 32 activations by v_dot2, 64 groups of a row a load.
 //
-// k_linear_few (T <= 4).  The 64 lanes hold 4 DIFFERENT groups of 16 rows, and a
-// product sums over all four: so the A operand is block diagonal, row 4 q + t =
-// token t in the lanes of group q and zero elsewhere.  The four products of the
-// four fragments then add up to D[4 q + t] = the sum of group q for token t, in
-// the very lane that loaded the group and its scale: no lane exchange, one scale
-// a lane and 4 scale FMAs for 32 codes.
+// k_linear_few (T = 2..4).  Matrix cores.  Products sum over the four lane rows,
+// which hold four DIFFERENT groups: so the A operand is block diagonal, row
+// 4 q + t = token t in the lanes of group q and zero elsewhere.  The products of
+// the four fragments then add up to D[4 q + t] = the sum of group q for token t,
+// in the very lane that has the group's scale: one scale and 4 scale FMAs for 32
+// codes a lane.  x stays in LDS for the whole launch.
 //
-// k_linear_mid (more tokens).  Tokens fill the 16 rows of A, so the four lanes of
-// a row must hold the same group: the fragments' words are transposed over the
-// four lane rows (4 swaps for 32 codes), the scales gathered (3 swaps).
+// k_linear_some (T = 5..16).  The tokens fill the 16 rows of A and the four lane
+// rows hold one group: 4 scale FMAs for 8 codes a lane.  x stays in LDS.
 //
-// The waves of a block split the groups of the same rows and join in LDS, in wave
-// order.
+// k_linear_tile (more tokens).  Tiles of 16 R rows a wave and 16 TT tokens, x
+// staged chunk by chunk; S parts of the waves split K and join in LDS.
+//
+// k_linear_mid: as k_linear_some with x read from the caches, the block's waves
+// splitting K: few rows, or x too large for LDS.
 #include "linear_frag.h"
 
 namespace moe {
 namespace {
 
-constexpr int kMaxWaves = 8;
-
-template <int QF> struct Weights {  // what a lane loads of one row tile: its group's codes and scale
-  typename CodeOf<QF>::T c;
-  uint16_t s, m;
-};
-
-template <int QF>
-__device__ __forceinline__ void load_w(const LinearArgs& a, int64_t group, Weights<QF>& w) {
-  using T = typename CodeOf<QF>::T;
-  typedef T Loose __attribute__((aligned(4)));
-  w.c = __builtin_nontemporal_load(reinterpret_cast<const Loose*>(a.codes + group * CodeOf<QF>::kBytes));
-  w.s = __builtin_nontemporal_load(a.scales + group);
-  if constexpr (QF == MOE_Q2_ASYM_G32) w.m = __builtin_nontemporal_load(a.mins + group);
-}
+constexpr int kChunk = 16;             // groups staged at once by the kernels with x in LDS
+constexpr size_t kLds = 160 * 1024;    // of a CU
+constexpr int kCus = 256;
 
 __device__ __forceinline__ void store_y(const LinearArgs& a, int t, int row, float v) {
   if (a.bias) v += a.bias[row];
@@ -46,97 +36,533 @@ __device__ __forceinline__ void store_y(const LinearArgs& a, int t, int row, flo
   else store_act<0>(a.y, at, v);
 }
 
-template <int QF, int ACT, int R>
-__global__ __launch_bounds__(64 * kMaxWaves) void k_linear_few(LinearArgs a) {
-  extern __shared__ float part[];  // [waves][16 R][4]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const int col = lane & 15, q = lane >> 4;
-  const int row0 = blockIdx.x * 16 * R;
+// ---------------------------------------------------------------- one token
+// LR lanes a row (64 / LR rows a load), NR loads in flight.
+template <int QF, int ACT, int LR, int NR>
+__global__ __launch_bounds__(256) void k_linear_one(LinearArgs a) {
+  constexpr int RPI = 64 / LR, kB = CodeOf<QF>::kBytes;
+  constexpr int kPlanes = QF == MOE_Q2_ASYM_G32 ? 2 : 1;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sub = lane / LR, gl = lane % LR;
   const int G = a.K / kGroup;
-  const int steps = (G + 3) >> 2;  // of 4 groups
-  const int j0 = steps * wave / waves, j1 = steps * (wave + 1) / waves;
-  const int t = col & 3;
-  const bool mine = (col >> 2) == q && t < a.T;  // this lane of A is not zero
-
-  int64_t base[R];  // first group of the lane's row in each tile (clamped: such rows are not stored)
+  const int row0 = (blockIdx.x * 4 + wave) * (NR * RPI);
+  if (row0 >= a.N) return;
+  const int64_t at = (int64_t)row0 * G, all = (int64_t)a.N * G;
+  const uint32_t left = (uint32_t)min(all - at, (int64_t)1 << 26);
+  const auto rc = rsrc(a.codes + at * kB, left * kB);
+  const auto rs = rsrc(a.scales + at, left * 2);
+  const auto rm = rsrc(kPlanes == 2 ? a.mins + at : a.scales, kPlanes == 2 ? left * 2 : 0);
+  const Unpack<QF> unpack;
+  float acc[NR] = {};
+  for (int g0 = 0; g0 < G; g0 += LR) {
+    const bool in = g0 + gl < G;
+    const int g = in ? g0 + gl : G - 1;
+    XHalf<ACT> xr[2];
 #pragma unroll
-  for (int r = 0; r < R; ++r) base[r] = (int64_t)min(row0 + 16 * r + col, a.N - 1) * G;
-
-  f32x4_v acc[R];
+    for (int h = 0; h < 2; ++h) xr[h] = load_half<ACT>(a.x, (size_t)g * kGroup + 16 * h);
+    typename CodeOf<QF>::T c[NR];
+    uint16_t s[NR], m[NR];
 #pragma unroll
-  for (int r = 0; r < R; ++r) acc[r] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-  const Frag off = offset_frag<QF>();
-
-#pragma unroll 2
-  for (int j = j0; j < j1; ++j) {
-    const int g = 4 * j + q;
-    const bool in = g < G;
-    const int gc = in ? g : G - 1;
-    XRaw<ACT> xr[4] = {};
-    if (mine && in) {
-#pragma unroll
-      for (int f = 0; f < 4; ++f) load_x<QF>(a.x, (size_t)t * a.ldx + g * kGroup + frag_first<QF>(f), xr[f]);
+    for (int r = 0; r < NR; ++r) {
+      const uint32_t o = (uint32_t)((r * RPI + sub) * G + g);
+      c[r] = buf_codes<QF>(rc, o * kB);
+      s[r] = __builtin_amdgcn_raw_buffer_load_b16(rs, o * 2, 0, 0);
+      if constexpr (kPlanes == 2) m[r] = __builtin_amdgcn_raw_buffer_load_b16(rm, o * 2, 0, 0);
     }
-    Weights<QF> w[R];
+    const float sx = half_sum(xr[0]) + half_sum(xr[1]);
+    Frag x[2][2][1];
+    if constexpr (ACT == MOE_ACT_BF16) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) load_w<QF>(a, base[r] + gc, w[r]);
-    Frag x[4][kParts<ACT>];
+      for (int h = 0; h < 2; ++h) half_frags<QF>(xr[h], x[h]);
+    }
 #pragma unroll
-    for (int f = 0; f < 4; ++f) x_frags(xr[f], x[f]);
-    f32x4_v c0 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-#pragma unroll
-      for (int p = 0; p < kParts<ACT>; ++p) c0 = mfma_frag(x[f][p], off, c0);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < NR; ++r) {
       uint32_t words[4];
-      frag_words<QF>(w[r].c, words);
-      f32x4_v d = c0;
+      frag_words<QF>(c[r], words);
+      float d = (QF == MOE_Q2_ASYM_G32 ? -1.f : -1.5f) * sx;
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        const Frag b = unpack_frag<QF>(words[f]);
+        const Frag b = unpack(words[f]);
 #pragma unroll
-        for (int p = 0; p < kParts<ACT>; ++p) d = mfma_frag(x[f][p], b, d);
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (ACT == MOE_ACT_BF16) {
+            d = dot2_bf16(b.d[j], x[f >> 1][f & 1][0].d[j], d);
+          } else {
+            const u32x4& xa = QF == MOE_Q4_SYM_G32 ? xr[f >> 1].v[2 * (f & 1)] : xr[f >> 1].v[f & 1];
+            const u32x4& xb = QF == MOE_Q4_SYM_G32 ? xr[f >> 1].v[2 * (f & 1) + 1] : xr[f >> 1].v[2 + (f & 1)];
+            d = fmaf(__uint_as_float(b.d[j] << 16), __uint_as_float(xa[j]), d);
+            d = fmaf(__uint_as_float(b.d[j] & 0xffff0000u), __uint_as_float(xb[j]), d);
+          }
+        }
       }
-      const float s = in ? f16_to_f32(w[r].s) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(s, d[i], acc[r][i]);
-      if constexpr (QF == MOE_Q2_ASYM_G32) {
-        const float m = in ? -0.25f * f16_to_f32(w[r].m) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(m, c0[i], acc[r][i]);
-      }
+      acc[r] = fmaf(in ? f16_to_f32(s[r]) : 0.f, d, acc[r]);
+      if constexpr (kPlanes == 2) acc[r] = fmaf(in ? 0.25f * f16_to_f32(m[r]) : 0.f, sx, acc[r]);
     }
   }
-
-  // the four groups of a step meet: sum over the lane rows
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t u, v;
-      swap16(__float_as_uint(acc[r][i]), &u, &v);
-      const float h = __uint_as_float(u) + __uint_as_float(v);
-      swap32(__float_as_uint(h), &u, &v);
-      acc[r][i] = __uint_as_float(u) + __uint_as_float(v);
-    }
-  if (q == 0) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[((wave * R + r) * 4 + i) * 16 + col] = acc[r][i];
-  }
-  __syncthreads();
-  for (int o = threadIdx.x; o < R * 64; o += blockDim.x) {  // o = (tile, token, row of the tile)
-    const int r = o >> 6, tok = (o >> 4) & 3, row = row0 + 16 * r + (o & 15);
-    if (tok >= a.T || row >= a.N) continue;
-    float v = 0.f;
-    for (int w = 0; w < waves; ++w) v += part[w * R * 64 + o];
-    store_y(a, tok, row, kOutFactor<QF> * v);
+  for (int r = 0; r < NR; ++r) {
+    const int row = row0 + r * RPI + sub;
+    const float v = seg_sum(acc[r], LR);
+    if (gl == 0 && row < a.N) store_y(a, 0, row, kOutFactor<QF> * v);
   }
 }
 
+template <int QF, int ACT, int LR>
+hipError_t run_one(const LinearArgs& a, hipStream_t s) {
+  constexpr int RPI = 64 / LR;
+  auto go = [&](auto nr) {
+    constexpr int NR = decltype(nr)::value, rows = 4 * NR * RPI;
+    k_linear_one<QF, ACT, LR, NR><<<(unsigned)((a.N + rows - 1) / rows), 256, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  // rows a wave: few while the chip is not full, many once it is
+  if (a.N <= 4096 * RPI) return go(std::integral_constant<int, 1>{});
+  if (a.N <= 65536 * RPI) return go(std::integral_constant<int, 4>{});
+  return go(std::integral_constant<int, 8>{});
+}
+
+// ---------------------------------------------------------------- two to four tokens
+// Blocks of 4 waves; a unit is 16 rows; S waves share a unit and split K.
+template <int QF, int ACT>
+struct FewLds {
+  static constexpr int P = kParts<ACT>;
+  int Tp, kQ, x, zero, c0, part, total;  // byte offsets behind the waves' weights
+  __host__ __device__ FewLds(int T, int chunks, int S) {
+    Tp = T == 3 ? 4 : T;
+    kQ = 17 * Tp * 16;  // 4 groups x 4 fragments x Tp tokens, padded
+    x = 4 * Stage<QF, 1, kChunk>::kBytes;
+    zero = x + P * chunks * 4 * kQ;
+    c0 = zero + 64;
+    part = c0 + chunks * kChunk * 16;
+    total = part + (S > 1 ? 1024 : 0);
+  }
+};
+
+template <int QF, int ACT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k_linear_few(LinearArgs a, int S, int units) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using St = Stage<QF, 1, kChunk>;
+  constexpr int P = kParts<ACT>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, q = lane >> 4;
+  const int G = a.K / kGroup, chunks = (G + kChunk - 1) / kChunk;
+  const FewLds<QF, ACT> L(a.T, chunks, S);
+  char* wl = lds + wave * St::kBytes;
+  char* xl = lds + L.x;
+  float* c0l = reinterpret_cast<float*>(lds + L.c0);
+  float* part = reinterpret_cast<float*>(lds + L.part);
+  const int tiles = 4 / S;  // units a block takes at a time
+  const int first_c = chunks * (wave % S) / S, nc = chunks * (wave % S + 1) / S - first_c;
+  const int first = blockIdx.x * tiles + wave / S, stride = gridDim.x * tiles;
+  const int rounds = (units - 1 - (int)blockIdx.x * tiles) / stride + 1;  // the same for every wave of the block
+
+  // x first, then the first weights: loads return in order, and x is wanted first
+  St w;
+  const int nx = a.T * chunks * kChunk * 2;
+  auto x_at = [&](int o, int* t, int* g) { *g = (o >> 1) % (chunks * kChunk); *t = (o >> 1) / (chunks * kChunk); };
+  auto x_load = [&](int o) {
+    int t, g;
+    x_at(o, &t, &g);
+    XHalf<ACT> r = {};
+    if (o < nx && g < G) r = load_half<ACT>(a.x, (size_t)t * a.ldx + g * kGroup + 16 * (o & 1));
+    return r;
+  };
+  constexpr int B = 2;
+  XHalf<ACT> xb[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) xb[b] = x_load(threadIdx.x + b * 256);
+  w.load(a, (int64_t)min(first, units - 1) * 16 * G + first_c * kChunk, true, lane);
+  for (int o0 = threadIdx.x; o0 < nx; o0 += B * 256) {
+    if (o0 >= B * 256) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) xb[b] = x_load(o0 + b * 256);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int o = o0 + b * 256;
+      if (o >= nx) break;
+      int t, g;
+      x_at(o, &t, &g);
+      Frag x[2][P];
+      half_frags<QF>(xb[b], x);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<Frag*>(xl + (p * (chunks * 4) + (g >> 2)) * L.kQ + (((g & 3) * 4 + 2 * (o & 1) + k) * L.Tp + t) * 16) = x[k][p];
+      const float sum = seg_sum(half_sum(xb[b]), 2);  // the two halves are neighbours
+      if ((o & 1) == 0) c0l[g * 4 + t] = (QF == MOE_Q2_ASYM_G32 ? -1.f : -1.5f) * sum;
+    }
+  }
+  for (int o = threadIdx.x; o < chunks * kChunk * 4; o += 256)
+    if ((o & 3) >= a.T) c0l[o] = 0.f;
+  if (threadIdx.x < 16) reinterpret_cast<uint32_t*>(lds + L.zero)[threadIdx.x] = 0;
+  __syncthreads();
+  const bool mine = (col >> 2) == q && (col & 3) < a.T;  // this lane of A is not zero
+  const char* xr = mine ? xl + q * L.kQ + (col & 3) * 16 : lds + L.zero;
+  const int xf = mine ? L.Tp * 16 : 16, xu = mine ? 4 * xf : 0, xc = mine ? 4 * L.kQ : 0, xp = mine ? chunks * 4 * L.kQ : 0;
+  const Unpack<QF> unpack;
+
+  for (int rd = 0; rd < rounds; ++rd) {
+    const int unit = first + rd * stride;
+    f32x4_v acc = {0.f, 0.f, 0.f, 0.f};
+    for (int cc = 0; cc < nc; ++cc) {
+      const int c = first_c + cc;
+      w.put(wl, G - c * kChunk, lane);
+      const bool end = cc + 1 == nc;
+      if (!end || rd + 1 < rounds) {
+        const int un = min(end ? unit + stride : unit, units - 1), cn = end ? first_c : c + 1;
+        w.load(a, (int64_t)un * 16 * G + cn * kChunk, true, lane);
+      }
+      // step u: lane row q works on group 4 q + u of the chunk, whose four scales lie together
+      const uint2 sc = *reinterpret_cast<const uint2*>(St::scale(wl, col, 4 * q));
+      const uint2 mn = St::kPlanes == 2 ? *reinterpret_cast<const uint2*>(St::scale(wl, col, 4 * q, 1)) : uint2{0, 0};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        __builtin_amdgcn_sched_barrier(0);  // (reads of all four steps at once would cost an occupancy step of registers)
+        Frag x[4][P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) x[f][p] = *reinterpret_cast<const Frag*>(xr + c * xc + p * xp + u * xu + f * xf);
+        const f32x4_v c0 = *reinterpret_cast<const f32x4_v*>(c0l + (c * kChunk + 4 * q + u) * 4);
+        const auto codes = *reinterpret_cast<const typename CodeOf<QF>::T*>(St::codes(wl, col, 4 * q + u));
+        uint32_t words[4];
+        frag_words<QF>(codes, words);
+        f32x4_v d = c0;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const Frag b = unpack(words[f]);
+#pragma unroll
+          for (int p = 0; p < P; ++p) d = mfma_frag(x[f][p], b, d);
+        }
+        const uint32_t sw = u < 2 ? sc.x : sc.y;
+        const float s = f16_to_f32((uint16_t)(u & 1 ? sw >> 16 : sw));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, d[i], acc[i]);
+        if constexpr (St::kPlanes == 2) {
+          const uint32_t mw = u < 2 ? mn.x : mn.y;
+          const float m = -0.25f * f16_to_f32((uint16_t)(u & 1 ? mw >> 16 : mw));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = fmaf(m, c0[i], acc[i]);
+        }
+      }
+    }
+    // the four groups of a step meet: sum over the lane rows; lane row t keeps token t
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t u, v;
+      swap16(__float_as_uint(acc[i]), &u, &v);
+      const float h = __uint_as_float(u) + __uint_as_float(v);
+      swap32(__float_as_uint(h), &u, &v);
+      acc[i] = __uint_as_float(u) + __uint_as_float(v);
+    }
+    const float v = q == 0 ? acc[0] : q == 1 ? acc[1] : q == 2 ? acc[2] : acc[3];
+    if (S == 1) {
+      const int row = unit * 16 + col;
+      if (q < a.T && row < a.N) store_y(a, q, row, kOutFactor<QF> * v);
+    } else {
+      __syncthreads();
+      part[wave * 64 + lane] = v;
+      __syncthreads();
+      if ((int)threadIdx.x < tiles * 64) {
+        const int row = ((int)blockIdx.x * tiles + wave + rd * stride) * 16 + col;
+        float t = 0.f;
+        for (int p = 0; p < S; ++p) t += part[(wave * S + p) * 64 + lane];
+        if (q < a.T && row < a.N) store_y(a, q, row, kOutFactor<QF> * t);
+      }
+    }
+  }
+}
+
+template <int QF, int ACT>
+bool few_fits(const LinearArgs& a) {
+  const int64_t chunks = (a.K / kGroup + kChunk - 1) / kChunk;
+  return FewLds<QF, ACT>(a.T, (int)chunks, 4).total <= (int)kLds;
+}
+template <int QF, int ACT>
+hipError_t run_few(const LinearArgs& a, hipStream_t s) {
+  const int units = (a.N + 15) / 16, chunks = (a.K / kGroup + kChunk - 1) / kChunk;
+  int S = 1;
+  while (S < 4 && units * S < 2048 && 2 * S <= chunks) S *= 2;
+  const int tiles = 4 / S, blocks = (units + tiles - 1) / tiles;
+  k_linear_few<QF, ACT><<<blocks < 4 * kCus ? blocks : 4 * kCus, 256, FewLds<QF, ACT>(a.T, chunks, S).total, s>>>(a, S, units);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- five to sixteen tokens
+template <int QF, int ACT, int W>
+__global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using St = Stage<QF, 1, kChunk>;
+  constexpr int P = kParts<ACT>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, q = lane >> 4;
+  const int G = a.K / kGroup, nc = (G + kChunk - 1) / kChunk;
+  char* wl = lds + wave * St::kBytes;
+  char* xl = lds + W * St::kBytes;  // [part][group][fragment][T | 1], then 16 zero bytes
+  const int ts = (a.T | 1) * 16, xpart = nc * kChunk * 4 * ts;
+  const int first = blockIdx.x * W + wave, stride = gridDim.x * W;
+  for (int o = threadIdx.x; o < nc * kChunk * 2; o += 64 * W) {  // half a group of every token
+    const int h = o & 1, g = o >> 1;
+    constexpr int B = 4;
+    for (int t0 = 0; t0 < a.T; t0 += B) {
+      XHalf<ACT> xb[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        xb[b] = XHalf<ACT>{};
+        if (g < G && t0 + b < a.T) xb[b] = load_half<ACT>(a.x, (size_t)(t0 + b) * a.ldx + g * kGroup + 16 * h);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (t0 + b >= a.T) break;
+        Frag x[2][P];
+        half_frags<QF>(xb[b], x);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            *reinterpret_cast<Frag*>(xl + p * xpart + (g * 4 + 2 * h + k) * ts + (t0 + b) * 16) = x[k][p];
+      }
+    }
+  }
+  if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(xl + P * xpart)[threadIdx.x] = 0;
+  St w;
+  if (first < units) w.load(a, (int64_t)first * 16 * G, true, lane);
+  __syncthreads();
+  const bool tok = col < a.T;
+  const char* xr = tok ? xl + q * ts + col * 16 : xl + P * xpart;
+  const int xg = tok ? 4 * ts : 0, xp = tok ? xpart : 0;
+  const Frag off = offset_frag<QF>();
+  const Unpack<QF> unpack;
+
+  for (int unit = first; unit < units; unit += stride) {
+    f32x4_v acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < nc; ++c) {
+      w.put(wl, G - c * kChunk, lane);
+      const bool end = c + 1 == nc;
+      if (!end || unit + stride < units)
+        w.load(a, (int64_t)(end ? unit + stride : unit) * 16 * G + (end ? 0 : c + 1) * kChunk, true, lane);
+      const char* xc = xr + c * kChunk * xg;
+#pragma unroll
+      for (int g4 = 0; g4 < kChunk; g4 += 4) {
+        const uint2 sc = *reinterpret_cast<const uint2*>(St::scale(wl, col, g4));
+        const uint2 mn = St::kPlanes == 2 ? *reinterpret_cast<const uint2*>(St::scale(wl, col, g4, 1)) : uint2{0, 0};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          Frag x[P];
+          f32x4_v c0 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            x[p] = *reinterpret_cast<const Frag*>(xc + p * xp + (g4 + u) * xg);
+            c0 = mfma_frag(x[p], off, c0);
+          }
+          const Frag b = unpack(lds_frag_word<QF>(St::codes(wl, col, g4 + u), q));
+          f32x4_v d = c0;
+#pragma unroll
+          for (int p = 0; p < P; ++p) d = mfma_frag(x[p], b, d);
+          const uint32_t sw = u < 2 ? sc.x : sc.y;
+          const float s = f16_to_f32((uint16_t)(u & 1 ? sw >> 16 : sw));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, d[i], acc[i]);
+          if constexpr (St::kPlanes == 2) {
+            const uint32_t mw = u < 2 ? mn.x : mn.y;
+            const float m = -0.25f * f16_to_f32((uint16_t)(u & 1 ? mw >> 16 : mw));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = fmaf(m, c0[i], acc[i]);
+          }
+        }
+      }
+    }
+    const int row = unit * 16 + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * q + i < a.T && row < a.N) store_y(a, 4 * q + i, row, kOutFactor<QF> * acc[i]);
+  }
+}
+
+template <int QF, int ACT, int W>
+size_t some_lds(const LinearArgs& a) {
+  const size_t nc = (a.K / kGroup + kChunk - 1) / kChunk;
+  return (size_t)W * Stage<QF, 1, kChunk>::kBytes + kParts<ACT> * nc * kChunk * 4 * (a.T | 1) * 16 + 16;
+}
+template <int QF, int ACT, int W>
+hipError_t run_some(const LinearArgs& a, hipStream_t s) {
+  const size_t lds = some_lds<QF, ACT, W>(a);
+  const int units = (a.N + 15) / 16, all = (units + W - 1) / W;
+  int per = (int)(kLds / lds);  // blocks a CU holds
+  if (per > 16 / W) per = 16 / W;
+  k_linear_some<QF, ACT, W><<<all < per * kCus ? all : per * kCus, 64 * W, lds, s>>>(a, units);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- token tiles
+template <int QF, int ACT, int R, int TT, int S>
+struct TileLds {
+  static constexpr int C = 8;
+  static constexpr int kX = kParts<ACT> * C * TT * 1024;  // x of a chunk
+  static constexpr int need = S * kX + 4 * S * Stage<QF, R, C>::kBytes;
+  static constexpr int join = (S - 1) * 4 * R * TT * 1024;
+  static constexpr int total = need > join ? need : join;
+  static_assert(total <= (int)kLds, "LDS");
+};
+
+template <int QF, int ACT, int R, int TT, int S, int OCC>
+__global__ __launch_bounds__(256 * S) __attribute__((amdgpu_waves_per_eu(OCC))) void k_linear_tile(LinearArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using L = TileLds<QF, ACT, R, TT, S>;
+  constexpr int C = L::C;
+  using St = Stage<QF, R, C>;
+  constexpr int P = kParts<ACT>, kXS = ACT == MOE_ACT_BF16 ? 2 : 4;
+  constexpr int XF = TT * C / 8;       // half groups a thread stages
+  constexpr int kTokStep = 128 / C;    // tokens a pass of a part's threads covers
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave >> 2, col = lane & 15, q = lane >> 4;
+  const int G = a.K / kGroup;
+  const int row0 = (blockIdx.x * 4 + (wave & 3)) * (16 * R), tok0 = blockIdx.y * (16 * TT);
+  const int chunks = (G + C - 1) / C, pc = (chunks + S - 1) / S, w0 = part * pc;  // chunks w0 .. w0 + pc - 1 are this part's
+  char* xl = lds + part * L::kX;
+  char* wl = lds + S * L::kX + wave * St::kBytes;
+
+  St w;
+  auto load_w = [&](int c) { w.load(a, (int64_t)row0 * G + (int64_t)(w0 + c) * C, w0 + c < chunks, lane); };
+  const int pt = threadIdx.x & 255, xh = pt & 1, xg = (pt >> 1) % C, xt = (pt >> 1) / C;
+  uint32_t xo[XF];  // byte offsets, past the end for tokens that are not there
+#pragma unroll
+  for (int i = 0; i < XF; ++i) {
+    const int t = xt + i * kTokStep;
+    xo[i] = tok0 + t < a.T ? (uint32_t)((t * a.ldx + xg * kGroup + 16 * xh) * kXS) : 0x80000000u;
+  }
+  const auto xrs = rsrc(reinterpret_cast<const char*>(a.x) + (int64_t)tok0 * a.ldx * kXS,
+                        (uint32_t)(((int64_t)(min(a.T - tok0, 16 * TT) - 1) * a.ldx + a.K) * kXS));
+  XHalf<ACT> xr[XF];
+  auto load_x = [&](int c) {
+    const bool in = (w0 + c) * C + xg < G;
+    const uint32_t go = (uint32_t)(w0 + c) * (C * kGroup * kXS);
+#pragma unroll
+    for (int i = 0; i < XF; ++i) {
+      const uint32_t o = in ? xo[i] + go : 0x80000000u;
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(xr[i].v) / 16); ++k) xr[i].v[k] = __builtin_amdgcn_raw_buffer_load_b128(xrs, o + 16 * k, 0, 0);
+    }
+  };
+  // a fragment's 16 tokens are rotated by a key of its half and group: writes (lanes
+  // of many groups, one token) and reads (lanes of many tokens, one group) both
+  // spread over the banks
+  auto put_x = [&]() {
+#pragma unroll
+    for (int i = 0; i < XF; ++i) {
+      const int t = xt + i * kTokStep;
+      Frag x[2][P];
+      half_frags<QF>(xr[i], x);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<Frag*>(xl + (((p * C + xg) * TT + (t >> 4)) * 64 + (2 * xh + k) * 16 + ((t & 15) ^ (xh * 8 + xg))) * 16) = x[k][p];
+    }
+  };
+
+  f32x4_v acc[R][TT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) acc[r][tt] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  const Frag off = offset_frag<QF>();
+  const Unpack<QF> unpack;
+
+  load_x(0);
+  load_w(0);
+  for (int c = 0; c < pc; ++c) {
+    if (c) __syncthreads();
+    put_x();
+    w.put(wl, G - (w0 + c) * C, lane);
+    if (c + 1 < pc) {
+      load_x(c + 1);
+      load_w(c + 1);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < C; ++g) {
+      Frag x[TT][P];
+      f32x4_v c0[TT];
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        c0[tt] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          x[tt][p] = *reinterpret_cast<const Frag*>(xl + (((p * C + g) * TT + tt) * 64 + q * 16 + (col ^ ((q >> 1) * 8 + g))) * 16);
+          c0[tt] = mfma_frag(x[tt][p], off, c0[tt]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const Frag b = unpack(lds_frag_word<QF>(St::codes(wl, 16 * r + col, g), q));
+        const float s = f16_to_f32(*reinterpret_cast<const uint16_t*>(St::scale(wl, 16 * r + col, g)));
+        float m = 0.f;
+        if constexpr (St::kPlanes == 2) m = -0.25f * f16_to_f32(*reinterpret_cast<const uint16_t*>(St::scale(wl, 16 * r + col, g, 1)));
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+          f32x4_v d = c0[tt];
+#pragma unroll
+          for (int p = 0; p < P; ++p) d = mfma_frag(x[tt][p], b, d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][tt][i] = fmaf(s, d[i], acc[r][tt][i]);
+          if constexpr (St::kPlanes == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][tt][i] = fmaf(m, c0[tt][i], acc[r][tt][i]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (S > 1) {  // parts meet: part 0 adds the others' sums, in order
+    float* j = reinterpret_cast<float*>(lds);
+    __syncthreads();
+    if (part > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+          *reinterpret_cast<f32x4_v*>(j + ((((part - 1) * 4 + (wave & 3)) * R + r) * TT + tt) * 256 + lane * 4) = acc[r][tt];
+    }
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int p = 0; p < S - 1; ++p)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+          acc[r][tt] += *reinterpret_cast<const f32x4_v*>(j + (((p * 4 + wave) * R + r) * TT + tt) * 256 + lane * 4);
+  }
+  auto write = [&](auto out) {
+    constexpr int OUT = decltype(out)::value;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = row0 + 16 * r + col;
+      const float bias = a.bias && row < a.N ? a.bias[row] : 0.f;
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = tok0 + 16 * tt + 4 * q + i;
+          if (t < a.T && row < a.N) store_act<OUT>(a.y, (size_t)t * a.ldy + row, fmaf(kOutFactor<QF>, acc[r][tt][i], bias));
+        }
+    }
+  };
+  if (a.out == MOE_ACT_BF16) write(std::integral_constant<int, MOE_ACT_BF16>{});
+  else write(std::integral_constant<int, MOE_ACT_F32>{});
+}
+
+template <int QF, int ACT, int R, int TT, int S, int OCC>
+hipError_t run_tile(const LinearArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N + 64 * R - 1) / (64 * R)), (unsigned)((a.T + 16 * TT - 1) / (16 * TT)));
+  k_linear_tile<QF, ACT, R, TT, S, OCC><<<grid, 256 * S, TileLds<QF, ACT, R, TT, S>::total, s>>>(a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- few rows
 // 4 x 4 transpose over (lane row of 16, register): p[g] of lane row q becomes p[q] of lane row g.
 __device__ __forceinline__ void transpose4(uint32_t (&p)[4]) {
   auto s16 = [](uint32_t& x, uint32_t& y) {
@@ -161,116 +587,87 @@ __device__ __forceinline__ void gather4(float v, float (&o)[4]) {
   o[0] = __uint_as_float(c); o[1] = __uint_as_float(e); o[2] = __uint_as_float(d); o[3] = __uint_as_float(f);
 }
 
-template <int QF, int ACT, int R, int TT>
-__global__ __launch_bounds__(64 * kMaxWaves) void k_linear_mid(LinearArgs a) {
-  extern __shared__ float part[];  // [waves][16 TT tokens][16 R rows]
+constexpr int kMidWaves = 8;
+
+template <int QF, int ACT>
+__global__ __launch_bounds__(64 * kMidWaves) void k_linear_mid(LinearArgs a) {
+  constexpr int kPlanes = QF == MOE_Q2_ASYM_G32 ? 2 : 1;
+  __shared__ float part[kMidWaves * 256];  // [wave][16 tokens][16 rows]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int col = lane & 15, q = lane >> 4;
-  const int row0 = blockIdx.x * 16 * R, tok0 = blockIdx.y * 16 * TT;
+  const int row0 = blockIdx.x * 16, tok0 = blockIdx.y * 16;
   const int G = a.K / kGroup;
-  const int steps = (G + 3) >> 2;
+  const int steps = (G + 3) >> 2;  // of 4 groups
   const int j0 = steps * wave / waves, j1 = steps * (wave + 1) / waves;
-
-  int64_t base[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) base[r] = (int64_t)min(row0 + 16 * r + col, a.N - 1) * G;
-  size_t xat[TT];  // tokens past the last read the last one's row and are not stored
-#pragma unroll
-  for (int tt = 0; tt < TT; ++tt)
-    xat[tt] = (size_t)min(tok0 + 16 * tt + col, a.T - 1) * a.ldx + frag_first<QF>(q);
-
-  f32x4_v acc[R][TT];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) acc[r][tt] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  // rows past the last and tokens past the last are computed from the last and not stored
+  const int64_t base = (int64_t)min(row0 + col, a.N - 1) * G;
+  const size_t xat = (size_t)min(tok0 + col, a.T - 1) * a.ldx + frag_first<QF>(q);
+  f32x4_v acc = {0.f, 0.f, 0.f, 0.f};
   const Frag off = offset_frag<QF>();
+  const Unpack<QF> unpack;
 
   for (int j = j0; j < j1; ++j) {
-    const int gq = min(4 * j + q, G - 1);
-    Weights<QF> w[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) load_w<QF>(a, base[r] + gq, w[r]);
-    uint32_t words[R][4];
-    float s[R][4], m[R][4];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      frag_words<QF>(w[r].c, words[r]);
-      transpose4(words[r]);
-      gather4(f16_to_f32(w[r].s), s[r]);
-      if constexpr (QF == MOE_Q2_ASYM_G32) gather4(-0.25f * f16_to_f32(w[r].m), m[r]);
-    }
+    const int64_t g0 = base + min(4 * j + q, G - 1);  // a lane row loads one group of the four
+    typedef typename CodeOf<QF>::T Code;
+    typedef Code Loose __attribute__((aligned(4)));
+    const Code c = *reinterpret_cast<const Loose*>(a.codes + g0 * CodeOf<QF>::kBytes);
+    uint32_t words[4];
+    float s[4], m[4];
+    frag_words<QF>(c, words);
+    transpose4(words);
+    gather4(f16_to_f32(a.scales[g0]), s);
+    if constexpr (kPlanes == 2) gather4(-0.25f * f16_to_f32(a.mins[g0]), m);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       if (4 * j + g < G) {  // the same for the whole wave
-        Frag b[R];
+        Frag x[kParts<ACT>];
+        load_frag<QF>(a.x, xat + (size_t)(4 * j + g) * kGroup, x);
+        const Frag b = unpack(words[g]);
+        f32x4_v c0 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < R; ++r) b[r] = unpack_frag<QF>(words[r][g]);
+        for (int p = 0; p < kParts<ACT>; ++p) c0 = mfma_frag(x[p], off, c0);
+        f32x4_v d = c0;
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-          XRaw<ACT> xr;
-          load_x<QF>(a.x, xat[tt] + (4 * j + g) * kGroup, xr);
-          Frag x[kParts<ACT>];
-          x_frags(xr, x);
-          f32x4_v c0 = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < kParts<ACT>; ++p) d = mfma_frag(x[p], b, d);
 #pragma unroll
-          for (int p = 0; p < kParts<ACT>; ++p) c0 = mfma_frag(x[p], off, c0);
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(s[g], d[i], acc[i]);
+        if constexpr (kPlanes == 2) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            f32x4_v d = c0;
-#pragma unroll
-            for (int p = 0; p < kParts<ACT>; ++p) d = mfma_frag(x[p], b[r], d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][tt][i] = fmaf(s[r][g], d[i], acc[r][tt][i]);
-            if constexpr (QF == MOE_Q2_ASYM_G32) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[r][tt][i] = fmaf(m[r][g], c0[i], acc[r][tt][i]);
-            }
-          }
+          for (int i = 0; i < 4; ++i) acc[i] = fmaf(m[g], c0[i], acc[i]);
         }
       }
     }
   }
 
-  constexpr int kOut = 256 * R * TT;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave * kOut + (16 * tt + 4 * q + i) * 16 * R + 16 * r + col] = acc[r][tt][i];
+  for (int i = 0; i < 4; ++i) part[wave * 256 + (4 * q + i) * 16 + col] = acc[i];
   __syncthreads();
-  for (int o = threadIdx.x; o < kOut; o += blockDim.x) {
-    const int tok = tok0 + o / (16 * R), row = row0 + o % (16 * R);
+  for (int o = threadIdx.x; o < 256; o += blockDim.x) {
+    const int tok = tok0 + (o >> 4), row = row0 + (o & 15);
     if (tok >= a.T || row >= a.N) continue;
     float v = 0.f;
-    for (int w = 0; w < waves; ++w) v += part[w * kOut + o];
+    for (int w = 0; w < waves; ++w) v += part[w * 256 + o];
     store_y(a, tok, row, kOutFactor<QF> * v);
   }
 }
 
-// Waves per block: enough waves on the chip, at least one step (4 groups) each.
-int split_waves(int64_t blocks, int G, int most) {
-  int w = 1;
-  while (w < most && blocks * w < 4096 && 2 * w <= (G + 3) / 4) w *= 2;
-  return w;
-}
-
-template <int QF, int ACT, int R>
-hipError_t run_few(const LinearArgs& a, hipStream_t s) {
-  const int64_t blocks = (a.N + 16 * R - 1) / (16 * R);
-  const int waves = split_waves(blocks, a.K / kGroup, kMaxWaves);
-  k_linear_few<QF, ACT, R><<<(unsigned)blocks, 64 * waves, waves * R * 64 * 4, s>>>(a);
-  return hipGetLastError();
-}
-
-template <int QF, int ACT, int R, int TT>
+template <int QF, int ACT>
 hipError_t run_mid(const LinearArgs& a, hipStream_t s) {
-  const int64_t bx = (a.N + 16 * R - 1) / (16 * R), by = (a.T + 16 * TT - 1) / (16 * TT);
-  constexpr int most = 65536 / (1024 * R * TT) < kMaxWaves ? 65536 / (1024 * R * TT) : kMaxWaves;  // 64 KiB of LDS
-  const int waves = split_waves(bx * by, a.K / kGroup, most);
-  k_linear_mid<QF, ACT, R, TT><<<dim3((unsigned)bx, (unsigned)by), 64 * waves, waves * R * TT * 1024, s>>>(a);
-  return hipGetLastError();
+  constexpr int kMaxY = 65535;
+  const int64_t bx = (a.N + 15) / 16;
+  for (int t0 = 0; t0 < a.T; t0 += 16 * kMaxY) {
+    LinearArgs b = a;
+    b.T = a.T - t0 < 16 * kMaxY ? a.T - t0 : 16 * kMaxY;
+    b.x = reinterpret_cast<const char*>(a.x) + (size_t)t0 * a.ldx * (ACT == MOE_ACT_BF16 ? 2 : 4);
+    b.y = reinterpret_cast<char*>(a.y) + (size_t)t0 * a.ldy * (a.out == MOE_ACT_BF16 ? 2 : 4);
+    const int64_t by = (b.T + 15) / 16;
+    int waves = 1;  // enough on the chip, at least one step (4 groups) each
+    while (waves < kMidWaves && bx * by * waves < 4096 && 2 * waves <= (a.K / kGroup + 3) / 4) waves *= 2;
+    k_linear_mid<QF, ACT><<<dim3((unsigned)bx, (unsigned)by), 64 * waves, 0, s>>>(b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -278,12 +675,41 @@ hipError_t run_mid(const LinearArgs& a, hipStream_t s) {
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   return by_qfmt(a.qfmt, [&](auto qf) {
     constexpr int QF = decltype(qf)::value;
+    auto one = [&](auto act, const LinearArgs& b) {
+      constexpr int ACT = decltype(act)::value;
+      const int G = b.K / kGroup;
+      if (G <= 8) return run_one<QF, ACT, 8>(b, s);
+      if (G <= 32) return run_one<QF, ACT, 32>(b, s);
+      return run_one<QF, ACT, 64>(b, s);
+    };
     auto go = [&](auto act) {
       constexpr int ACT = decltype(act)::value;
-      if (a.T <= 4) return a.N > 16384 ? run_few<QF, ACT, 2>(a, s) : run_few<QF, ACT, 1>(a, s);
-      if (a.T <= 16) return a.N > 16384 ? run_mid<QF, ACT, 4, 1>(a, s) : run_mid<QF, ACT, 1, 1>(a, s);
-      if (a.T <= 32) return a.N > 8192 ? run_mid<QF, ACT, 4, 2>(a, s) : run_mid<QF, ACT, 2, 2>(a, s);
-      return run_mid<QF, ACT, 4, 4>(a, s);
+      if (a.T == 1) return one(act, a);
+      if (a.T <= 4) {
+        if (few_fits<QF, ACT>(a)) return run_few<QF, ACT>(a, s);
+        for (int t = 0; t < a.T; ++t) {  // x too large for LDS: token by token
+          LinearArgs b = a;
+          b.T = 1;
+          b.x = reinterpret_cast<const char*>(a.x) + (size_t)t * a.ldx * (ACT == MOE_ACT_BF16 ? 2 : 4);
+          b.y = reinterpret_cast<char*>(a.y) + (size_t)t * a.ldy * (a.out == MOE_ACT_BF16 ? 2 : 4);
+          const hipError_t e = one(act, b);
+          if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+      }
+      if (a.T <= 16) {
+        if (a.N >= 8192 && some_lds<QF, ACT, 8>(a) <= kLds) return run_some<QF, ACT, 8>(a, s);
+        return run_mid<QF, ACT>(a, s);
+      }
+      if (64 * a.ldx * (ACT == MOE_ACT_BF16 ? 2 : 4) >= (int64_t)1 << 31) return run_mid<QF, ACT>(a, s);
+      const int64_t r64 = (a.N + 63) / 64, t64 = (a.T + 63) / 64;
+      if constexpr (ACT == MOE_ACT_BF16) {
+        if (r64 * t64 >= 1024) return run_tile<QF, ACT, 2, 4, 1, 2>(a, s);
+        if (r64 * t64 >= 192) return run_tile<QF, ACT, 1, 4, 2, 2>(a, s);
+        return run_tile<QF, ACT, 1, 2, 4, 4>(a, s);
+      } else {
+        return run_tile<QF, ACT, 1, 2, 2, 2>(a, s);
+      }
     };
     if (a.act == MOE_ACT_BF16) return go(std::integral_constant<int, MOE_ACT_BF16>{});
     return go(std::integral_constant<int, MOE_ACT_F32>{});

@@ -20,6 +20,9 @@ DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 SIZES = [(1, 1, 32), (1, 17, 96), (1, 300, 2048), (2, 33, 64), (3, 100, 160), (4, 70, 2048), (5, 129, 2016), (8, 64, 768),
          (13, 257, 224), (16, 100, 1024), (17, 61, 544), (33, 130, 512), (64, 96, 4096), (65, 200, 160), (130, 257, 96),
          (300, 129, 2080)]
+# sizes that take the kernels of many rows: several rounds of a block, tiles of two row groups, x that does not fit LDS
+MANY = [(1, 70001, 96), (3, 40001, 64), (4, 33, 20000), (6, 8200, 96), (16, 9001, 544), (12, 8200, 1664), (130, 4200, 96),
+        (1030, 4100, 64)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -103,7 +106,7 @@ def test_exact_sums(qfmt, act):
     """Inputs whose every partial sum fits 24 bits: y equals the definition bit
     for bit, so no weight or activation lost a bit on the way.  (bf16: at most
     12 x 2 x 2047 x 31 < 2^24 units of 2^-14; fp32: 2^18 x 31 < 2^23 units.)"""
-    for i, (T, n, k) in enumerate(SIZES):
+    for i, (T, n, k) in enumerate(SIZES + MANY):
         gu.say(f"linear exact {qfmt} {act} T={T} N={n} K={k}")
         c = Case(qfmt, n, k, 100 + i, True, act, bias=False)
         x = sparse_x(np.random.default_rng(i), T, k, act)
@@ -131,6 +134,20 @@ def test_random_values(qfmt, act, out):
             lim = lim + 2.0 ** -24 * (np.abs(want) + lim)
         worst = (np.abs(y - want) / lim).max()
         assert worst <= 1.0, (T, n, k, worst)
+
+
+@pytest.mark.parametrize("act", ("bf16", "f32"))
+@pytest.mark.parametrize("qfmt", FORMATS)
+def test_random_values_many_rows(qfmt, act):
+    for i, (T, n, k) in enumerate(MANY):
+        gu.say(f"linear random {qfmt} {act} T={T} N={n} K={k}")
+        r = np.random.default_rng(700 + i)
+        c = Case(qfmt, n, k, 300 + i, False, act, "f32")
+        x = mo.round_act(0.3 + r.standard_normal((T, k)), act)
+        y = call(c, c.x_dev(x), T).cpu().numpy().astype(np.float64)
+        want = c.ref(x)
+        lim = c.bound(x)
+        assert (np.abs(y - want) <= lim + 2.0 ** -24 * (np.abs(want) + lim)).all(), (T, n, k)
 
 
 @pytest.mark.parametrize("T", (1, 4, 7, 40, 130))
