@@ -285,13 +285,12 @@ typedef struct moe_beam {
  *   L_r         = log sum_{v in A_r} exp(logits[r][v])
  *   total(w, v) = scores[b][w] + (logits[r][v] - L_r)          (in 64 bits)
  * A beam with finished_opt[b][w] != 0 has the one candidate (w, eos) with
- * total scores[b][w]; its logits are not read.  A row whose score or L_r is not
+ * total scores[b][w], whatever its logits are.  A row whose score or L_r is not
  * finite (nothing allowed, a NaN or +inf among the allowed logits, a score of
  * -inf) has no candidates, and a logit of -inf is none.
  * out_parent / out_token / out_score [B][n_out] receive the n_out candidates of
- * the largest total, in descending order, equal totals by the lower w V + v
- * (within a beam the order is that of the logits); out_score is the total
- * rounded to fp32.  Where there are fewer candidates the rest are
+ * the largest total, in descending order, equal totals by the lower w V + v;
+ * out_score is the total rounded to fp32.  Where there are fewer candidates the rest are
  * (-1, -1, -inf).  Results do not depend on the launch or on other rows.
  * Workspace: at least moe_beam_workspace_bytes(beam), 256-byte aligned. */
 moe_status moe_beam_select(const moe_beam *beam, const void *logits, int64_t logits_stride, const float *scores,

@@ -1,11 +1,20 @@
 // Beam search: the n best continuations of each sequence over beams and
 // vocabulary, and the move of the beams' states to follow their parents.
 //
-// Selection.  k_beam_rows: one block per beam evaluates L = log sum exp over
-// the allowed logits (maximum, then the sum of exp(l - max) in 64 bits) and
-// picks the row's n largest logits one after the other (equal logits: lower
-// token).  k_beam_merge: one block per sequence picks the n largest of the
-// beams' candidates by total = score + (logit - L) in 64 bits.
+// Selection, two kernels.  A row's vocabulary is cut into segments of 512
+// consecutive tokens.
+//
+// k_beam_scan reads every logit once: a wave takes U segments of a row and writes
+// each segment's maximum and, over the U segments, (m, sum exp(l - m)).  No
+// selection happens here: the n best candidates of a sequence lie in the n
+// segments whose maxima are best (in the order of the totals, equal ones by
+// index: if n other segments come before a candidate's, each holds an element
+// that comes before the candidate).  The sum is held, and exp evaluated, in 64
+// bits: totals of different beams lie within 1e-7 of each other now and then, and
+// an L good to 1e-10 keeps them in order.
+//
+// k_beam_pick, one block per sequence: L of every beam, the n best segments, then
+// the n best elements of those (read again, from the caches).
 #include "moe_device.h"
 #include "moe_internal.h"
 #include "topk.h"
@@ -14,87 +23,152 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSeg = 512;  // tokens of a segment
 
-struct RowList {   // workspace of one selection
-  double* lse;     // [B*W], NaN: the row has no candidates
-  uint64_t* keys;  // [B*W][n] sel_key(logit, token), 0 past the last
+// ---------------------------------------------------------------- scan
+struct BeamWs {
+  double* sum;   // [rows][units]
+  float* top;    // [rows][units]
+  float* seg;    // [rows][segs] maxima
+  int units, segs;
 };
 
-__host__ __device__ inline RowList row_list(void* ws, int rows) {
-  const size_t at = ((size_t)rows * 8 + 255) & ~(size_t)255;
-  return RowList{reinterpret_cast<double*>(ws), reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ws) + at)};
+__host__ __device__ inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+__host__ __device__ inline BeamWs beam_ws(void* ws, int rows, int V, int U) {
+  BeamWs w;
+  w.segs = (V + kSeg - 1) / kSeg;
+  w.units = (w.segs + U - 1) / U;
+  char* p = reinterpret_cast<char*>(ws);
+  w.sum = reinterpret_cast<double*>(p);
+  p += up256((size_t)rows * w.units * 8);
+  w.top = reinterpret_cast<float*>(p);
+  p += up256((size_t)rows * w.units * 4);
+  w.seg = reinterpret_cast<float*>(p);
+  return w;
 }
 
-__device__ __forceinline__ bool allowed(const BeamArgs& a, int row, int v) {
-  return !a.allowed || ((a.allowed[(size_t)row * a.ld_allowed + (v >> 5)] >> (v & 31)) & 1u);
+// exp(d) for d <= 0 to 2e-10 (relative): d = n ln 2 + y with |y| <= ln 2 / 2 + 2^-13,
+// the series of e^y to y^8 / 8!, n into the exponent.  Below -700 it stops
+// falling (1e-304, nothing next to the maximum's 1); NaN stays NaN.
+__device__ __forceinline__ double exp_down(double d) {
+  d = d < -700.0 ? -700.0 : d;
+  const float n = rintf((float)d * 1.44269504f);
+  const double y = fma(-(double)n, 0.69314718055994530942, d);
+  double p = 1.0 / 40320;
+  p = fma(p, y, 1.0 / 5040);
+  p = fma(p, y, 1.0 / 720);
+  p = fma(p, y, 1.0 / 120);
+  p = fma(p, y, 1.0 / 24);
+  p = fma(p, y, 1.0 / 6);
+  p = fma(p, y, 0.5);
+  p = fma(p, y, 1.0);
+  p = fma(p, y, 1.0);
+  return __hiloint2double(__double2hiint(p) + ((int)n << 20), __double2loint(p));
 }
 
-// (+ 0: a negative zero equals a positive one and must not sort below it)
+__device__ __forceinline__ float wave_max_f(float v) {
+  v = fmaxf(v, dpp_f<kDppXor1>(v));
+  v = fmaxf(v, dpp_f<kDppXor2>(v));
+  v = fmaxf(v, dpp_f<kDppHalfMirror>(v));
+  v = fmaxf(v, dpp_f<kDppMirror>(v));
+  uint32_t a, b;
+  swap16(__float_as_uint(v), &a, &b);
+  v = fmaxf(__uint_as_float(a), __uint_as_float(b));
+  swap32(__float_as_uint(v), &a, &b);
+  return fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+
+// Bits of the allowed mask for n (4 or 8) tokens from v on (v a multiple of n).
+__device__ __forceinline__ uint32_t allowed_bits(const BeamArgs& a, int row, int v) {
+  return a.allowed[(size_t)row * a.ld_allowed + (v >> 5)] >> (v & 31);
+}
+
+// 8 logits of one lane of segment s: tokens s 512 + 4 lane + {0..3} and the same + 256
+// (fp32) or s 512 + 8 lane + {0..7} (bf16); tokens that are not there or not
+// allowed are -inf.  (+ 0 makes a negative zero positive: the two are equal.)
 template <int ACT>
-__device__ __forceinline__ float logit(const BeamArgs& a, int row, int v) {
-  return allowed(a, row, v) ? load_act<ACT>(a.logits, (size_t)row * a.ld + v) + 0.0f : -INFINITY;
-}
-
-// Block-wide maximum of a 64-bit key / sum of a double (every thread gets it).
-__device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* sh) {
-  v = wave_max_u64(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  for (int i = 0; i < kThreads / 64; ++i) v = sh[i] > v ? sh[i] : v;
-  return v;
-}
-__device__ __forceinline__ double block_sum(double v, double* sh) {
-  __syncthreads();
-  sh[threadIdx.x] = v;
-  __syncthreads();
-  for (int s = kThreads / 2; s > 0; s >>= 1) {
-    if ((int)threadIdx.x < s) sh[threadIdx.x] += sh[threadIdx.x + s];
-    __syncthreads();
-  }
-  return sh[0];
-}
-
-template <int ACT>
-__global__ __launch_bounds__(kThreads) void k_beam_rows(BeamArgs a) {
-  __shared__ double dsh[kThreads];
-  __shared__ uint64_t ksh[kThreads / 64];
-  const int row = blockIdx.x;
-  if (a.finished && a.finished[row]) return;  // its one candidate needs no logits
-  const RowList out = row_list(a.ws, a.B * a.W);
-  uint64_t best = 0;
-  bool bad = false;
-  for (int v = threadIdx.x; v < a.V; v += kThreads) {
-    const float l = logit<ACT>(a, row, v);
-    if (l != l || l == INFINITY) bad = true;
-    const uint64_t k = sel_key(l, v);
-    best = k > best ? k : best;
-  }
-  const bool any_bad = __syncthreads_or(bad);
-  best = block_max(best, ksh);
-  const float top = key_value((uint32_t)(best >> 32));
-  const bool none = any_bad || top == -INFINITY;
-  double sum = 0.0;
-  if (!none)
-    for (int v = threadIdx.x; v < a.V; v += kThreads) sum += exp((double)logit<ACT>(a, row, v) - (double)top);
-  sum = block_sum(sum, dsh);
-  if (threadIdx.x == 0) out.lse[row] = none ? __longlong_as_double(0x7ff8000000000000ll) : (double)top + log(sum);
-  if (none) return;
-  for (int i = 0; i < a.n; ++i) {
-    if (threadIdx.x == 0) out.keys[(size_t)row * a.n + i] = best;
-    if (best == 0) continue;
-    const uint64_t last = best;
-    best = 0;
-    for (int v = threadIdx.x; v < a.V; v += kThreads) {
-      const float l = logit<ACT>(a, row, v);
-      const uint64_t k = l == -INFINITY ? 0 : sel_key(l, v);
-      if (k < last && k > best) best = k;
+__device__ __forceinline__ void load_seg(const BeamArgs& a, int row, int s, int lane, float (&v)[8]) {
+  constexpr int N = ACT == MOE_ACT_BF16 ? 8 : 4;
+#pragma unroll
+  for (int h = 0; h < 8 / N; ++h) {
+    const int t = s * kSeg + 256 * h + N * lane;
+    const size_t at = (size_t)row * a.ld + t;
+    if (t + N <= a.V) {
+      if constexpr (ACT == MOE_ACT_BF16) {
+        typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+        const u32x4_any r = *reinterpret_cast<const u32x4_any*>(reinterpret_cast<const uint16_t*>(a.logits) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = __uint_as_float(r[i] << 16);
+          v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        }
+      } else {
+        typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+        const f32x4_any r = *reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(a.logits) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * h + i] = r[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[N * h + i] = t + i < a.V ? load_act<ACT>(a.logits, at + i) : -INFINITY;
     }
-    best = block_max(best, ksh);
+    if (a.allowed && t < a.V) {
+      const uint32_t bits = allowed_bits(a, row, t);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!((bits >> i) & 1)) v[N * h + i] = -INFINITY;
+    }
   }
 }
 
-// Order-preserving map of a double (never NaN here).
+template <int ACT, int U>
+__global__ __launch_bounds__(kThreads) void k_beam_scan(BeamArgs a, int64_t work) {
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= work) return;
+  const BeamWs w = beam_ws(a.ws, a.B * a.W, a.V, U);
+  const int row = (int)(id / w.units), unit = (int)(id % w.units);
+  if (a.finished && a.finished[row]) return;  // its one candidate needs no logits
+  float v[U][8], top = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = -INFINITY;
+    if (unit * U + u < w.segs) load_seg<ACT>(a, row, unit * U + u, lane, v[u]);
+  }
+  float mine = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float m = v[u][0];  // (fmaxf passes over a NaN; the sum keeps it)
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, v[u][i]);
+    m = wave_max_f(m);
+    if (lane == u) mine = m;
+    top = fmaxf(top, m);
+  }
+  if (lane < U && unit * U + lane < w.segs) w.seg[(size_t)row * w.segs + unit * U + lane] = mine + 0.0f;
+  // all -inf: the sum is 0, but for a NaN, which has to be seen
+  const double base = top == -INFINITY ? 0.0 : (double)top;
+  double sum = 0.0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double e = exp_down((double)v[u][i] - base);
+      sum += v[u][i] == -INFINITY ? 0.0 : e;
+    }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+  if (lane == 0) {
+    const size_t at = (size_t)row * w.units + unit;
+    w.sum[at] = sum;
+    w.top[at] = top;
+  }
+}
+
+// ---------------------------------------------------------------- pick
+// Order-preserving map of a double (never NaN here); every real value is > 0.
 __device__ __forceinline__ uint64_t order_key64(double d) {
   const uint64_t u = (uint64_t)__double_as_longlong(d);
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
@@ -103,95 +177,284 @@ __device__ __forceinline__ double key64_value(uint64_t k) {
   return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
-// Candidate i of beam w: its total (as an ordered key, 0: none) and token.
-__device__ __forceinline__ uint64_t candidate(const BeamArgs& a, const RowList& in, int row, int i, int* token) {
-  const float s = a.scores[row];
-  if (!(s > -INFINITY && s < INFINITY)) return 0;
-  if (a.finished && a.finished[row]) {
-    *token = a.eos;
-    return i == 0 ? order_key64((double)s) : 0;
-  }
-  const double L = in.lse[row];
-  if (L != L) return 0;
-  const uint64_t k = in.keys[(size_t)row * a.n + i];
-  if (k == 0) return 0;
-  *token = key_id(k);
-  return order_key64((double)s + ((double)key_value((uint32_t)(k >> 32)) - L));
+// A candidate: the larger total first, equal totals by the lower index.  key 0: none.
+struct Cand { uint64_t key; uint32_t idx; };
+__device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
+  return a.key > b.key || (a.key == b.key && a.idx < b.idx);
 }
 
-__global__ __launch_bounds__(kThreads) void k_beam_merge(BeamArgs a) {
-  __shared__ uint64_t ksh[kThreads / 64];
-  const int b = blockIdx.x;
-  const RowList in = row_list(a.ws, a.B * a.W);
-  const int total = a.W * a.n;
-  uint64_t last = ~0ull;
-  uint32_t last_flat = 0;
-  for (int o = 0; o < a.n; ++o) {
-    // the largest key below (last, last_flat) in the order (key desc, flat asc)
-    uint64_t best = 0;
-    for (int c = threadIdx.x; c < total; c += kThreads) {
-      int token = 0;
-      const int w = c / a.n;
-      const uint64_t k = candidate(a, in, b * a.W + w, c % a.n, &token);
-      const uint32_t flat = (uint32_t)w * (uint32_t)a.V + (uint32_t)token;
-      if (k && (k < last || (k == last && flat > last_flat)) && k > best) best = k;
+constexpr int kCap = 1024;  // candidates held between two rankings
+struct PickLds {
+  uint64_t key[kCap];
+  uint32_t idx[kCap];
+  uint64_t out_key[128];
+  uint32_t out_idx[128];
+  uint32_t head[kThreads];
+  uint32_t count, edge;
+};
+
+// The held candidates ranked (everyone counts those before it); the n first stay,
+// in order.  Returns how many there are.
+__device__ int rank_held(PickLds& L, int n) {
+  __syncthreads();
+  const int m = (int)L.count;
+  for (int i = threadIdx.x; i < m; i += kThreads) {
+    const Cand c{L.key[i], L.idx[i]};
+    int r = 0;
+    for (int j = 0; j < m; ++j) r += before(Cand{L.key[j], L.idx[j]}, c);
+    if (r < n) { L.out_key[r] = c.key; L.out_idx[r] = c.idx; }
+  }
+  __syncthreads();
+  const int k = m < n ? m : n;
+  for (int i = threadIdx.x; i < k; i += kThreads) { L.key[i] = L.out_key[i]; L.idx[i] = L.out_idx[i]; }
+  if (threadIdx.x == 0) L.count = k;
+  __syncthreads();
+  return k;
+}
+
+constexpr int kHeld = 32;  // values a thread holds: 8192 candidates are read once
+
+// The n first of `total` candidates (load(i) the value from memory, cand(i, value)
+// the candidate; different indices), in order, in L.key / L.idx; returns how many
+// there are.
+//   A first pass takes each thread's best and the n-th best of those: at least n
+// candidates are as good, so nothing worse is held in the second pass (by the
+// upper 32 bits of the key; usually little more than n candidates remain).  When
+// the held ones do not fit, as with many equal totals, they are ranked 256 at a
+// time and only what comes before the n-th of them is held from there on.
+template <typename Load, typename Make>
+__device__ int block_select(PickLds& L, int n, int total, Load&& load, Make&& cand) {
+  constexpr int kBatch = kThreads * kHeld;
+  float v[kHeld];
+  auto read = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      if (i0 + k * kThreads >= total) break;  // (the same for the whole block)
+      v[k] = load(min(i0 + k * kThreads + (int)threadIdx.x, total - 1));
     }
-    best = block_max(best, ksh);
-    uint64_t low = 0;  // lowest flat index at that key, as ~flat + 1
-    if (best)
-      for (int c = threadIdx.x; c < total; c += kThreads) {
-        int token = 0;
-        const int w = c / a.n;
-        const uint64_t k = candidate(a, in, b * a.W + w, c % a.n, &token);
-        const uint32_t flat = (uint32_t)w * (uint32_t)a.V + (uint32_t)token;
-        if (k == best && (k < last || flat > last_flat)) {
-          const uint64_t inv = (uint64_t)(0xffffffffu - flat) + 1;
-          low = inv > low ? inv : low;
+  };
+  uint32_t best = 0;
+  for (int i0 = 0; i0 < total; i0 += kBatch) {
+    read(i0);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      if (i0 + k * kThreads >= total) break;
+      const int i = i0 + k * kThreads + (int)threadIdx.x;
+      const uint32_t h = i < total ? (uint32_t)(cand(i, v[k]).key >> 32) : 0u;
+      best = h > best ? h : best;
+    }
+  }
+  __syncthreads();
+  L.head[threadIdx.x] = best;
+  if (threadIdx.x == 0) { L.count = 0; L.edge = 0; }
+  __syncthreads();
+  {
+    int more = 0, least = 0;  // threads with a better best; with one at least as good
+    const uint4* h4 = reinterpret_cast<const uint4*>(L.head);
+#pragma unroll 8
+    for (int j = 0; j < kThreads / 4; ++j) {
+      const uint4 h = h4[j];
+      more += (h.x > best) + (h.y > best) + (h.z > best) + (h.w > best);
+      least += (h.x >= best) + (h.y >= best) + (h.z >= best) + (h.w >= best);
+    }
+    if (more < n && least >= n) L.edge = best;  // (the n-th: every thread that gets here has the same)
+  }
+  __syncthreads();
+  const uint32_t edge = L.edge;
+  Cand last{0, 0xffffffffu};  // the n-th held so far
+  for (int i0 = 0; i0 < total; i0 += kBatch) {
+    if (total > kBatch) read(i0);
+    auto passes = [&](int i, int k, Cand* c) {
+      if (i >= total) return false;
+      *c = cand(i, v[k]);
+      return c->key && (uint32_t)(c->key >> 32) >= edge && before(*c, last);
+    };
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      if (i0 + k * kThreads >= total) break;
+      Cand c;
+      mine += passes(i0 + k * kThreads + (int)threadIdx.x, k, &c);
+    }
+    const uint32_t held = L.count;
+    __syncthreads();
+    uint32_t at = mine ? atomicAdd(&L.count, mine) : 0u;
+    __syncthreads();
+    const bool fits = L.count <= (uint32_t)kCap;
+    __syncthreads();
+    if (fits) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        if (i0 + k * kThreads >= total) break;
+        Cand c;
+        if (passes(i0 + k * kThreads + (int)threadIdx.x, k, &c)) {
+          L.key[at] = c.key;
+          L.idx[at++] = c.idx;
         }
       }
-    low = block_max(low, ksh);
-    const size_t at = (size_t)b * a.n + o;
-    const uint32_t flat = 0xffffffffu - (uint32_t)(low - 1);
-    if (threadIdx.x == 0) {
-      a.out_score[at] = best ? (float)key64_value(best) : -INFINITY;
-      a.out_parent[at] = best ? (int)(flat / (uint32_t)a.V) : -1;
-      a.out_token[at] = best ? (int)(flat % (uint32_t)a.V) : -1;
+      __syncthreads();
+    } else {
+      if (threadIdx.x == 0) L.count = held;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        if (i0 + k * kThreads >= total) break;
+        if (L.count > kCap - kThreads) {  // (the same for the whole block)
+          if (rank_held(L, n) == n) last = Cand{L.key[n - 1], L.idx[n - 1]};
+        }
+        __syncthreads();
+        Cand c;
+        if (passes(i0 + k * kThreads + (int)threadIdx.x, k, &c)) {
+          const uint32_t to = atomicAdd(&L.count, 1u);
+          L.key[to] = c.key;
+          L.idx[to] = c.idx;
+        }
+        __syncthreads();
+      }
+      if (rank_held(L, n) == n) last = Cand{L.key[n - 1], L.idx[n - 1]};
     }
-    last = best;
-    last_flat = flat;
-    if (!best) last = 0;
+  }
+  return rank_held(L, n);
+}
+
+template <int ACT, int U>
+__global__ __launch_bounds__(kThreads) void k_beam_pick(BeamArgs a) {
+  __shared__ __attribute__((aligned(16))) PickLds L;
+  __shared__ double lse[64], score[64];  // lse NaN: the beam has no candidates
+  __shared__ uint8_t over[64];           // finished beams
+  __shared__ int2 chosen[128];           // beam and first token of the best segments
+  const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const BeamWs w = beam_ws(a.ws, a.B * a.W, a.V, U);
+  for (int i = wave; i < a.W; i += kThreads / 64) {
+    const int row = b * a.W + i;
+    const float sc = a.scores[row];
+    double l = __longlong_as_double(0x7ff8000000000000ll);
+    if (a.finished && a.finished[row]) {
+      l = 0.0;
+    } else {
+      float top = -INFINITY;
+      for (int u = lane; u < w.units; u += 64) top = fmaxf(top, w.top[(size_t)row * w.units + u]);
+      top = wave_max_f(top);
+      const double base = top == -INFINITY ? 0.0 : (double)top;
+      double sum = 0.0;
+      for (int u = lane; u < w.units; u += 64) {
+        const float t = w.top[(size_t)row * w.units + u];
+        const double s = w.sum[(size_t)row * w.units + u];
+        sum += t == -INFINITY ? s : s * exp_down((double)t - base);
+      }
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+      if (top > -INFINITY && top < INFINITY) l = (double)top + log(sum);  // NaN if a logit was
+    }
+    if (!(sc > -INFINITY && sc < INFINITY)) l = __longlong_as_double(0x7ff8000000000000ll);
+    if (lane == 0) {
+      lse[i] = l;
+      score[i] = (double)sc;
+      over[i] = a.finished && a.finished[row];
+    }
+  }
+  __syncthreads();
+  auto total_key = [&](int beam, float v) -> uint64_t {
+    const double l = lse[beam];
+    if (l != l || v == -INFINITY) return 0;
+    return order_key64(score[beam] + ((double)v - l));
+  };
+  // the best segments: index beam * segs + segment; a finished beam has its token's segment only
+  const int n_seg = block_select(
+      L, a.n, a.W * w.segs,
+      [&](int i) { return w.seg[(size_t)b * a.W * w.segs + i]; },
+      [&](int i, float v) {
+        const int beam = i / w.segs;
+        if (over[beam]) v = i % w.segs == a.eos / kSeg ? 0.f : -INFINITY;
+        return Cand{total_key(beam, v), (uint32_t)i};
+      });
+  for (int i = threadIdx.x; i < n_seg; i += kThreads) {
+    const int beam = (int)L.idx[i] / w.segs;
+    chosen[i] = make_int2(beam, ((int)L.idx[i] % w.segs) * kSeg);
+  }
+  __syncthreads();
+  // the best of their elements: index beam * V + token
+  const int n_out = block_select(
+      L, a.n, n_seg * kSeg,
+      [&](int i) {
+        const int2 g = chosen[i / kSeg];
+        const int t = min(g.y + i % kSeg, a.V - 1), row = b * a.W + g.x;
+        const float v = load_act<ACT>(a.logits, (size_t)row * a.ld + t) + 0.0f;
+        return a.allowed && !(allowed_bits(a, row, t) & 1) ? -INFINITY : v;
+      },
+      [&](int i, float v) {
+        const int2 g = chosen[i / kSeg];
+        const int t = g.y + i % kSeg;
+        if (over[g.x]) v = t == a.eos ? 0.f : -INFINITY;
+        return Cand{t < a.V ? total_key(g.x, v) : 0, (uint32_t)g.x * (uint32_t)a.V + (uint32_t)t};
+      });
+  for (int i = threadIdx.x; i < a.n; i += kThreads) {
+    const size_t at = (size_t)b * a.n + i;
+    const bool have = i < n_out;
+    a.out_score[at] = have ? (float)key64_value(L.key[i]) : -INFINITY;
+    a.out_parent[at] = have ? (int)(L.idx[i] / (uint32_t)a.V) : -1;
+    a.out_token[at] = have ? (int)(L.idx[i] % (uint32_t)a.V) : -1;
   }
 }
 
 // ---------------------------------------------------------------- reordering
-constexpr int kStates = 32;  // states per launch (the descriptors travel as kernel arguments)
+constexpr int kStates = 32;       // states per launch (the descriptors travel as kernel arguments)
+constexpr int kMaxBlocks = 1 << 16;  // of one state and sequence
 
 struct StateArgs {
   moe_state s[kStates];
+  uint32_t end[kStates];  // blocks up to and with this state
   const int32_t* parent;
   int64_t ldp;
-  int W;
+  int W, n;
 };
 
-// Block (x, sequence, state): each thread owns columns (byte positions) of
-// every row of one sequence, reads the column of all parents before it writes
-// any, and nobody else touches that column, so dst may be src.
+// A thread owns a column (the same B bytes of every row) of one sequence: it reads
+// the column of all parents before it writes any, and nobody else touches that
+// column, so dst may be src, and a row that is its own parent is left alone there.
+// Block (x, sequence); x runs over the states' columns.
+template <int B, int WB>
 __global__ __launch_bounds__(kThreads) void k_reorder(StateArgs a) {
-  const moe_state& s = a.s[blockIdx.z];
+  typedef uint32_t Words __attribute__((ext_vector_type(B >= 8 ? B / 4 : 2)));
+  using V = std::conditional_t<B >= 8, Words, std::conditional_t<B == 4, uint32_t, uint8_t>>;
+  int k = 0;
+  while (k + 1 < a.n && blockIdx.x >= a.end[k]) ++k;
+  const moe_state& s = a.s[k];
+  const uint32_t first = k ? a.end[k - 1] : 0u;
   const int b = blockIdx.y;
-  const int64_t total = s.chunks * s.chunk_bytes;
+  const bool same = s.src == s.dst;
   const char* src = reinterpret_cast<const char*>(s.src) + (int64_t)b * a.W * s.src_row_stride;
   char* dst = reinterpret_cast<char*>(s.dst) + (int64_t)b * a.W * s.dst_row_stride;
-  for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < total; c += (int64_t)gridDim.x * kThreads) {
-    const int64_t piece = c / s.chunk_bytes, off = c % s.chunk_bytes;
-    char v[64];
-    for (int i = 0; i < a.W; ++i) {
-      const int p = a.parent[b * a.ldp + i];
-      v[i] = p >= 0 && p < a.W ? src[p * s.src_row_stride + piece * s.src_chunk_stride + off] : 0;
+  const int64_t piece = s.chunk_bytes / B, total = s.chunks * piece;
+  const int64_t step = (int64_t)(a.end[k] - first) * kThreads;
+  const int32_t* parent = a.parent + b * a.ldp;
+  for (int64_t c = (int64_t)(blockIdx.x - first) * kThreads + threadIdx.x; c < total; c += step) {
+    int64_t pc = 0, off = c;
+    if (s.chunks > 1) {
+      if (total <= 0x7fffffff) {  // 32-bit division where it does
+        pc = (uint32_t)c / (uint32_t)piece;
+        off = (uint32_t)c % (uint32_t)piece;
+      } else {
+        pc = c / piece;
+        off = c % piece;
+      }
     }
-    for (int i = 0; i < a.W; ++i) {
-      const int p = a.parent[b * a.ldp + i];
-      if (p >= 0 && p < a.W) dst[i * s.dst_row_stride + piece * s.dst_chunk_stride + off] = v[i];
+    const char* from = src + pc * s.src_chunk_stride + off * B;
+    char* to = dst + pc * s.dst_chunk_stride + off * B;
+    V v[WB];
+#pragma unroll
+    for (int i = 0; i < WB; ++i) {
+      if (i < a.W) {
+        const int p = parent[i];
+        if ((uint32_t)p < (uint32_t)a.W && !(same && p == i)) v[i] = *reinterpret_cast<const V*>(from + p * s.src_row_stride);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < WB; ++i) {
+      if (i < a.W) {
+        const int p = parent[i];
+        if ((uint32_t)p < (uint32_t)a.W && !(same && p == i)) *reinterpret_cast<V*>(to + i * s.dst_row_stride) = v[i];
+      }
     }
   }
 }
@@ -199,49 +462,80 @@ __global__ __launch_bounds__(kThreads) void k_reorder(StateArgs a) {
 }  // namespace
 
 size_t beam_ws_bytes(int B, int W, int V, int n, int act) {
-  (void)V; (void)act;
-  const size_t rows = (size_t)B * W;
-  return ((rows * 8 + 255) & ~(size_t)255) + ((rows * n * 8 + 255) & ~(size_t)255);
+  (void)n; (void)act;
+  const size_t rows = (size_t)B * W, segs = (V + kSeg - 1) / kSeg;  // one segment a unit at most
+  return up256(rows * segs * 8) + 2 * up256(rows * segs * 4);
 }
 
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
-  const unsigned rows = (unsigned)(a.B * a.W);
-  if (a.act == MOE_ACT_BF16) k_beam_rows<MOE_ACT_BF16><<<rows, kThreads, 0, s>>>(a);
-  else k_beam_rows<MOE_ACT_F32><<<rows, kThreads, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  k_beam_merge<<<(unsigned)a.B, kThreads, 0, s>>>(a);
-  return hipGetLastError();
+  const int64_t rows = (int64_t)a.B * a.W, segs = (a.V + kSeg - 1) / kSeg;
+  auto go = [&](auto act, auto u) {
+    constexpr int ACT = decltype(act)::value, U = decltype(u)::value;
+    const int64_t work = rows * ((segs + U - 1) / U), blocks = (work + kThreads / 64 - 1) / (kThreads / 64);
+    k_beam_scan<ACT, U><<<(unsigned)blocks, kThreads, 0, s>>>(a, work);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_beam_pick<ACT, U><<<(unsigned)a.B, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  auto units = [&](auto act) {
+    // four segments a wave read 8 KiB at once; one while that leaves the chip idle
+    if (rows * segs >= 8192) return go(act, std::integral_constant<int, 4>{});
+    return go(act, std::integral_constant<int, 1>{});
+  };
+  if (a.act == MOE_ACT_BF16) return units(std::integral_constant<int, MOE_ACT_BF16>{});
+  return units(std::integral_constant<int, MOE_ACT_F32>{});
 }
 
 hipError_t launch_beam_reorder(const moe_state* states, int n, const int32_t* parent, int64_t ldp, int B, int W,
                                hipStream_t s) {
+  // the widest column that every address, stride and size of a state allows
+  auto width = [&](const moe_state& st) {
+    uint64_t all = reinterpret_cast<uintptr_t>(st.src) | reinterpret_cast<uintptr_t>(st.dst) | (uint64_t)st.chunk_bytes |
+                   (uint64_t)st.src_row_stride | (uint64_t)st.dst_row_stride | (uint64_t)st.src_chunk_stride |
+                   (uint64_t)st.dst_chunk_stride;
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
+  };
+  auto run = [&](auto bytes, const StateArgs& a, int blocks, int nb) {
+    constexpr int BY = decltype(bytes)::value;
+    const dim3 grid((unsigned)blocks, (unsigned)nb);
+    if (W <= 8) k_reorder<BY, 8><<<grid, kThreads, 0, s>>>(a);
+    else if (W <= 16) k_reorder<BY, 16><<<grid, kThreads, 0, s>>>(a);
+    else if (W <= 32) k_reorder<BY, 32><<<grid, kThreads, 0, s>>>(a);
+    else k_reorder<BY < 16 ? BY : 8, 64><<<grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+  };
   for (int b0 = 0; b0 < B; b0 += 65535) {
     const int nb = B - b0 < 65535 ? B - b0 : 65535;
-    StateArgs a{};
-    a.parent = parent + b0 * ldp;
-    a.ldp = ldp;
-    a.W = W;
-    int m = 0;
-    int64_t most = 0;
-    for (int i = 0; i < n; ++i) {
-      moe_state st = states[i];
-      if (st.chunk_bytes && st.chunks) {
-        if (B * W == 1) st.src_row_stride = st.dst_row_stride = 0;
-        if (st.chunks == 1) st.src_chunk_stride = st.dst_chunk_stride = 0;
-        st.src = reinterpret_cast<const char*>(st.src) + (int64_t)b0 * W * st.src_row_stride;
-        st.dst = reinterpret_cast<char*>(st.dst) + (int64_t)b0 * W * st.dst_row_stride;
-        most = st.chunks * st.chunk_bytes > most ? st.chunks * st.chunk_bytes : most;
-        a.s[m++] = st;
-      }
-      if (m == kStates || (i == n - 1 && m > 0)) {
-        const int64_t want = (most + kThreads - 1) / kThreads;
-        const dim3 grid((unsigned)(want < 1024 ? want : 1024), (unsigned)nb, (unsigned)m);
-        k_reorder<<<grid, kThreads, 0, s>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        m = 0;
-        most = 0;
+    for (int bytes = 16; bytes >= 1; bytes /= 4) {  // one launch for up to kStates states of a width
+      const int col = bytes == 16 && W > 32 ? 8 : bytes;
+      StateArgs a{};
+      a.parent = parent + b0 * ldp;
+      a.ldp = ldp;
+      a.W = W;
+      int64_t blocks = 0;
+      for (int i = 0; i <= n; ++i) {
+        if (i < n) {
+          moe_state st = states[i];
+          if (st.chunk_bytes == 0 || st.chunks == 0) continue;
+          if (B * W == 1) st.src_row_stride = st.dst_row_stride = 0;
+          if (st.chunks == 1) st.src_chunk_stride = st.dst_chunk_stride = 0;
+          if (width(st) != bytes) continue;
+          st.src = reinterpret_cast<const char*>(st.src) + (int64_t)b0 * W * st.src_row_stride;
+          st.dst = reinterpret_cast<char*>(st.dst) + (int64_t)b0 * W * st.dst_row_stride;
+          const int64_t want = (st.chunks * st.chunk_bytes / col + kThreads - 1) / kThreads;
+          blocks += want < kMaxBlocks ? want : kMaxBlocks;
+          a.s[a.n] = st;
+          a.end[a.n++] = (uint32_t)blocks;
+        }
+        if (a.n == kStates || (i == n && a.n > 0)) {
+          const hipError_t e = bytes == 16  ? run(std::integral_constant<int, 16>{}, a, (int)blocks, nb)
+                               : bytes == 4 ? run(std::integral_constant<int, 4>{}, a, (int)blocks, nb)
+                                            : run(std::integral_constant<int, 1>{}, a, (int)blocks, nb);
+          if (e != hipSuccess) return e;
+          a.n = 0;
+          blocks = 0;
+        }
       }
     }
   }
