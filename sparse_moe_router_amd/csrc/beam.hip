@@ -48,13 +48,16 @@ __host__ __device__ inline BeamWs beam_ws(void* ws, int rows, int V, int U) {
   return w;
 }
 
-// exp(d) for d <= 0 to 2e-10 (relative): d = n ln 2 + y with |y| <= ln 2 / 2 + 2^-13,
-// the series of e^y to y^8 / 8!, n into the exponent.  Below -700 it stops
-// falling (1e-304, nothing next to the maximum's 1); NaN stays NaN.
-__device__ __forceinline__ double exp_down(double d) {
-  d = d < -700.0 ? -700.0 : d;
-  const float n = rintf((float)d * 1.44269504f);
-  const double y = fma(-(double)n, 0.69314718055994530942, d);
+// exp(v - top) to 2e-10 (relative) for v <= top, top finite; what lies more than 700
+// below counts e^-700, nothing next to the top's 1.  v - top = n ln 2 + y with |y| <=
+// ln 2 / 2 (and what n, rounded from an fp32 product, may be off: 2^-13), the series
+// of e^y to y^8 / 8!, n into the exponent.  n comes as the low bits of n + 1.5 2^23,
+// where the sum rounds to a whole number.
+__device__ __forceinline__ double exp_below(float v, float top) {
+  constexpr float kWhole = 12582912.f;
+  const float m = fmaf(fmaxf(v - top, -700.f), 1.44269504f, kWhole);
+  const double d = fmax((double)v - (double)top, -700.0);
+  const double y = fma(-(double)(m - kWhole), 0.69314718055994530942, d);
   double p = 1.0 / 40320;
   p = fma(p, y, 1.0 / 5040);
   p = fma(p, y, 1.0 / 720);
@@ -64,7 +67,7 @@ __device__ __forceinline__ double exp_down(double d) {
   p = fma(p, y, 0.5);
   p = fma(p, y, 1.0);
   p = fma(p, y, 1.0);
-  return __hiloint2double(__double2hiint(p) + ((int)n << 20), __double2loint(p));
+  return __hiloint2double(__double2hiint(p) + (__float_as_int(m) << 20), __double2loint(p));
 }
 
 __device__ __forceinline__ float wave_max_f(float v) {
@@ -77,6 +80,25 @@ __device__ __forceinline__ float wave_max_f(float v) {
   v = fmaxf(__uint_as_float(a), __uint_as_float(b));
   swap32(__float_as_uint(v), &a, &b);
   return fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+  return v + __hiloint2double((int)dpp_u<CTRL>((uint32_t)__double2hiint(v)), (int)dpp_u<CTRL>((uint32_t)__double2loint(v)));
+}
+// Sum over the wave, the same bits in every lane.
+__device__ __forceinline__ double wave_sum_d(double v) {
+  v = add_dpp<kDppXor1>(v);
+  v = add_dpp<kDppXor2>(v);
+  v = add_dpp<kDppHalfMirror>(v);
+  v = add_dpp<kDppMirror>(v);
+  uint32_t h0, h1, l0, l1;
+  swap16((uint32_t)__double2hiint(v), &h0, &h1);
+  swap16((uint32_t)__double2loint(v), &l0, &l1);
+  v = __hiloint2double((int)h0, (int)l0) + __hiloint2double((int)h1, (int)l1);
+  swap32((uint32_t)__double2hiint(v), &h0, &h1);
+  swap32((uint32_t)__double2loint(v), &l0, &l1);
+  return __hiloint2double((int)h0, (int)l0) + __hiloint2double((int)h1, (int)l1);
 }
 
 // Bits of the allowed mask for n (4 or 8) tokens from v on (v a multiple of n).
@@ -138,31 +160,33 @@ __global__ __launch_bounds__(kThreads) void k_beam_scan(BeamArgs a, int64_t work
     if (unit * U + u < w.segs) load_seg<ACT>(a, row, unit * U + u, lane, v[u]);
   }
   float mine = 0.f;
+  bool bad = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float m = v[u][0];  // (fmaxf passes over a NaN; the sum keeps it)
+    float m = v[u][0];  // (fmaxf passes over a NaN)
+    bad |= v[u][0] != v[u][0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, v[u][i]);
+    for (int i = 1; i < 8; ++i) {
+      m = fmaxf(m, v[u][i]);
+      bad |= v[u][i] != v[u][i];
+    }
     m = wave_max_f(m);
     if (lane == u) mine = m;
     top = fmaxf(top, m);
   }
   if (lane < U && unit * U + lane < w.segs) w.seg[(size_t)row * w.segs + unit * U + lane] = mine + 0.0f;
-  // all -inf: the sum is 0, but for a NaN, which has to be seen
-  const double base = top == -INFINITY ? 0.0 : (double)top;
   double sum = 0.0;
+  if (top > -INFINITY && top < INFINITY) {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double e = exp_down((double)v[u][i] - base);
-      sum += v[u][i] == -INFINITY ? 0.0 : e;
-    }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+      for (int i = 0; i < 8; ++i) sum += exp_below(v[u][i], top);
+    sum = wave_sum_d(sum);
+  }
+  bad = __any(bad) || top == INFINITY;
   if (lane == 0) {
     const size_t at = (size_t)row * w.units + unit;
-    w.sum[at] = sum;
+    w.sum[at] = bad ? __longlong_as_double(0x7ff8000000000000ll) : sum;
     w.top[at] = top;
   }
 }
@@ -183,98 +207,123 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
   return a.key > b.key || (a.key == b.key && a.idx < b.idx);
 }
 
-constexpr int kCap = 1024;  // candidates held between two rankings
+constexpr int kPick = 1024;  // threads of k_beam_pick
+constexpr int kCap = 2048;  // candidates held between two rankings
 struct PickLds {
   uint64_t key[kCap];
   uint32_t idx[kCap];
   uint64_t out_key[128];
   uint32_t out_idx[128];
-  uint32_t head[kThreads];
+  uint32_t head[kPick / 4];
   uint32_t count, edge;
 };
 
-// The held candidates ranked (everyone counts those before it); the n first stay,
-// in order.  Returns how many there are.
+// The held candidates ranked (16 lanes each, counting those before it); the n first
+// stay, in order.  Returns how many there are.
 __device__ int rank_held(PickLds& L, int n) {
   __syncthreads();
   const int m = (int)L.count;
-  for (int i = threadIdx.x; i < m; i += kThreads) {
-    const Cand c{L.key[i], L.idx[i]};
+  for (int i0 = 0; i0 < m; i0 += kPick / 16) {
+    const int i = i0 + (int)(threadIdx.x >> 4);
+    const Cand c{L.key[min(i, m - 1)], L.idx[min(i, m - 1)]};
     int r = 0;
-    for (int j = 0; j < m; ++j) r += before(Cand{L.key[j], L.idx[j]}, c);
-    if (r < n) { L.out_key[r] = c.key; L.out_idx[r] = c.idx; }
+#pragma unroll 4
+    for (int j = threadIdx.x & 15; j < m; j += 16) r += before(Cand{L.key[j], L.idx[j]}, c);
+    r += (int)dpp_u<kDppXor1>((uint32_t)r);
+    r += (int)dpp_u<kDppXor2>((uint32_t)r);
+    r += (int)dpp_u<kDppHalfMirror>((uint32_t)r);
+    r += (int)dpp_u<kDppMirror>((uint32_t)r);
+    if (i < m && r < n && (threadIdx.x & 15) == 0) { L.out_key[r] = c.key; L.out_idx[r] = c.idx; }
   }
   __syncthreads();
   const int k = m < n ? m : n;
-  for (int i = threadIdx.x; i < k; i += kThreads) { L.key[i] = L.out_key[i]; L.idx[i] = L.out_idx[i]; }
+  for (int i = threadIdx.x; i < k; i += kPick) { L.key[i] = L.out_key[i]; L.idx[i] = L.out_idx[i]; }
   if (threadIdx.x == 0) L.count = k;
   __syncthreads();
   return k;
 }
 
-constexpr int kHeld = 32;  // values a thread holds: 8192 candidates are read once
+constexpr int kHeld = 8;  // values a thread holds: 8192 candidates are read once
 
 // The n first of `total` candidates (load(i) the value from memory, cand(i, value)
 // the candidate; different indices), in order, in L.key / L.idx; returns how many
-// there are.
-//   A first pass takes each thread's best and the n-th best of those: at least n
-// candidates are as good, so nothing worse is held in the second pass (by the
-// upper 32 bits of the key; usually little more than n candidates remain).  When
-// the held ones do not fit, as with many equal totals, they are ranked 256 at a
+// there are.  ready() runs once the first values are on their way.  floor: if not
+// 0, at least n candidates are known to have keys with upper halves >= floor.
+//   A first pass takes the best of every four threads and the n-th best of those: at
+// least n candidates are as good, so nothing worse is held in the second pass (by
+// the upper 32 bits of the key; usually little more than n candidates remain).  When
+// the held ones do not fit, as with many equal totals, they are ranked 1024 at a
 // time and only what comes before the n-th of them is held from there on.
-template <typename Load, typename Make>
-__device__ int block_select(PickLds& L, int n, int total, Load&& load, Make&& cand) {
-  constexpr int kBatch = kThreads * kHeld;
+template <typename Load, typename Ready, typename Make>
+__device__ int block_select(PickLds& L, int n, int total, uint32_t floor, Load&& load, Ready&& ready, Make&& cand) {
+  constexpr int kBatch = kPick * kHeld;
   float v[kHeld];
+  uint32_t h[kHeld];
   auto read = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
-      if (i0 + k * kThreads >= total) break;  // (the same for the whole block)
-      v[k] = load(min(i0 + k * kThreads + (int)threadIdx.x, total - 1));
+      if (i0 + k * kPick >= total) break;  // (the same for the whole block)
+      v[k] = load(min(i0 + k * kPick + (int)threadIdx.x, total - 1));
+    }
+  };
+  auto heads = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      h[k] = 0;
+      if (i0 + k * kPick >= total) continue;
+      const int i = i0 + k * kPick + (int)threadIdx.x;
+      if (i < total) h[k] = (uint32_t)(cand(i, v[k]).key >> 32);
     }
   };
   uint32_t best = 0;
   for (int i0 = 0; i0 < total; i0 += kBatch) {
     read(i0);
+    if (i0 == 0) ready();
+    if (floor && total > kBatch) break;  // (read and looked at below)
+    heads(i0);
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      if (i0 + k * kThreads >= total) break;
-      const int i = i0 + k * kThreads + (int)threadIdx.x;
-      const uint32_t h = i < total ? (uint32_t)(cand(i, v[k]).key >> 32) : 0u;
-      best = h > best ? h : best;
-    }
+    for (int k = 0; k < kHeld; ++k) best = max(best, h[k]);
   }
-  __syncthreads();
-  L.head[threadIdx.x] = best;
-  if (threadIdx.x == 0) { L.count = 0; L.edge = 0; }
-  __syncthreads();
-  {
-    int more = 0, least = 0;  // threads with a better best; with one at least as good
-    const uint4* h4 = reinterpret_cast<const uint4*>(L.head);
+  if (threadIdx.x == 0) { L.count = 0; L.edge = floor; }
+  if (!floor) {
+    best = max(best, dpp_u<kDppXor1>(best));
+    best = max(best, dpp_u<kDppXor2>(best));
+    if ((threadIdx.x & 3) == 0) L.head[threadIdx.x >> 2] = best;
+    __syncthreads();
+    // heads that are better, that are at least as good: each of the four threads counts a quarter
+    int more = 0, least = 0;
+    const uint4* h4 = reinterpret_cast<const uint4*>(L.head) + (threadIdx.x & 3) * (kPick / 64);
 #pragma unroll 8
-    for (int j = 0; j < kThreads / 4; ++j) {
-      const uint4 h = h4[j];
-      more += (h.x > best) + (h.y > best) + (h.z > best) + (h.w > best);
-      least += (h.x >= best) + (h.y >= best) + (h.z >= best) + (h.w >= best);
+    for (int j = 0; j < kPick / 64; ++j) {
+      const uint4 o = h4[j];
+      more += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
+      least += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
     }
+    more += (int)dpp_u<kDppXor1>((uint32_t)more);
+    more += (int)dpp_u<kDppXor2>((uint32_t)more);
+    least += (int)dpp_u<kDppXor1>((uint32_t)least);
+    least += (int)dpp_u<kDppXor2>((uint32_t)least);
     if (more < n && least >= n) L.edge = best;  // (the n-th: every thread that gets here has the same)
   }
   __syncthreads();
-  const uint32_t edge = L.edge;
+  const uint32_t edge = max(L.edge, 1u);  // (key 0 is no candidate)
   Cand last{0, 0xffffffffu};  // the n-th held so far
   for (int i0 = 0; i0 < total; i0 += kBatch) {
-    if (total > kBatch) read(i0);
-    auto passes = [&](int i, int k, Cand* c) {
-      if (i >= total) return false;
+    if (total > kBatch) {
+      read(i0);
+      heads(i0);
+    }
+    auto passes = [&](int k, Cand* c) {
+      if (h[k] < edge) return false;
+      const int i = i0 + k * kPick + (int)threadIdx.x;
       *c = cand(i, v[k]);
-      return c->key && (uint32_t)(c->key >> 32) >= edge && before(*c, last);
+      return before(*c, last);
     };
     uint32_t mine = 0;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
-      if (i0 + k * kThreads >= total) break;
       Cand c;
-      mine += passes(i0 + k * kThreads + (int)threadIdx.x, k, &c);
+      mine += passes(k, &c);
     }
     const uint32_t held = L.count;
     __syncthreads();
@@ -283,13 +332,14 @@ __device__ int block_select(PickLds& L, int n, int total, Load&& load, Make&& ca
     const bool fits = L.count <= (uint32_t)kCap;
     __syncthreads();
     if (fits) {
+      if (mine) {
 #pragma unroll
-      for (int k = 0; k < kHeld; ++k) {
-        if (i0 + k * kThreads >= total) break;
-        Cand c;
-        if (passes(i0 + k * kThreads + (int)threadIdx.x, k, &c)) {
-          L.key[at] = c.key;
-          L.idx[at++] = c.idx;
+        for (int k = 0; k < kHeld; ++k) {
+          Cand c;
+          if (passes(k, &c)) {
+            L.key[at] = c.key;
+            L.idx[at++] = c.idx;
+          }
         }
       }
       __syncthreads();
@@ -298,13 +348,12 @@ __device__ int block_select(PickLds& L, int n, int total, Load&& load, Make&& ca
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
-        if (i0 + k * kThreads >= total) break;
-        if (L.count > kCap - kThreads) {  // (the same for the whole block)
+        if (L.count > kCap - kPick) {  // (the same for the whole block)
           if (rank_held(L, n) == n) last = Cand{L.key[n - 1], L.idx[n - 1]};
         }
         __syncthreads();
         Cand c;
-        if (passes(i0 + k * kThreads + (int)threadIdx.x, k, &c)) {
+        if (passes(k, &c)) {
           const uint32_t to = atomicAdd(&L.count, 1u);
           L.key[to] = c.key;
           L.idx[to] = c.idx;
@@ -318,42 +367,44 @@ __device__ int block_select(PickLds& L, int n, int total, Load&& load, Make&& ca
 }
 
 template <int ACT, int U>
-__global__ __launch_bounds__(kThreads) void k_beam_pick(BeamArgs a) {
+__global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a) {
   __shared__ __attribute__((aligned(16))) PickLds L;
   __shared__ double lse[64], score[64];  // lse NaN: the beam has no candidates
   __shared__ uint8_t over[64];           // finished beams
   __shared__ int2 chosen[128];           // beam and first token of the best segments
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const BeamWs w = beam_ws(a.ws, a.B * a.W, a.V, U);
-  for (int i = wave; i < a.W; i += kThreads / 64) {
-    const int row = b * a.W + i;
-    const float sc = a.scores[row];
-    double l = __longlong_as_double(0x7ff8000000000000ll);
-    if (a.finished && a.finished[row]) {
-      l = 0.0;
-    } else {
-      float top = -INFINITY;
-      for (int u = lane; u < w.units; u += 64) top = fmaxf(top, w.top[(size_t)row * w.units + u]);
-      top = wave_max_f(top);
-      const double base = top == -INFINITY ? 0.0 : (double)top;
-      double sum = 0.0;
-      for (int u = lane; u < w.units; u += 64) {
-        const float t = w.top[(size_t)row * w.units + u];
-        const double s = w.sum[(size_t)row * w.units + u];
-        sum += t == -INFINITY ? s : s * exp_down((double)t - base);
+  const double none = __longlong_as_double(0x7ff8000000000000ll);
+  auto beams = [&]() {
+    for (int i = wave; i < a.W; i += kPick / 64) {
+      const int row = b * a.W + i;
+      const float sc = a.scores[row];
+      const bool fin = a.finished && a.finished[row];
+      double l = 0.0;
+      if (!fin) {
+        float top = -INFINITY;  // of the lane's units so far, and their sum relative to it
+        double sum = 0.0;
+        for (int u = lane; u < w.units; u += 64) {
+          const float t = w.top[(size_t)row * w.units + u];
+          const double su = w.sum[(size_t)row * w.units + u];  // (0 for a unit of -inf, NaN for one with a NaN)
+          const float m = fmaxf(top, t);
+          sum = sum * exp_below(top, m) + su * exp_below(t, m);
+          top = m;
+        }
+        const float all = wave_max_f(top);
+        sum = wave_sum_d(sum * exp_below(top, all));
+        top = all;
+        l = top > -INFINITY && top < INFINITY ? (double)top + log(sum) : none;
       }
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-      if (top > -INFINITY && top < INFINITY) l = (double)top + log(sum);  // NaN if a logit was
+      if (!(sc > -INFINITY && sc < INFINITY)) l = none;
+      if (lane == 0) {
+        lse[i] = l;
+        score[i] = (double)sc;
+        over[i] = fin;
+      }
     }
-    if (!(sc > -INFINITY && sc < INFINITY)) l = __longlong_as_double(0x7ff8000000000000ll);
-    if (lane == 0) {
-      lse[i] = l;
-      score[i] = (double)sc;
-      over[i] = a.finished && a.finished[row];
-    }
-  }
-  __syncthreads();
+    __syncthreads();
+  };
   auto total_key = [&](int beam, float v) -> uint64_t {
     const double l = lse[beam];
     if (l != l || v == -INFINITY) return 0;
@@ -361,34 +412,36 @@ __global__ __launch_bounds__(kThreads) void k_beam_pick(BeamArgs a) {
   };
   // the best segments: index beam * segs + segment; a finished beam has its token's segment only
   const int n_seg = block_select(
-      L, a.n, a.W * w.segs,
-      [&](int i) { return w.seg[(size_t)b * a.W * w.segs + i]; },
+      L, a.n, a.W * w.segs, 0u,
+      [&](int i) { return w.seg[(size_t)b * a.W * w.segs + i]; }, beams,
       [&](int i, float v) {
         const int beam = i / w.segs;
         if (over[beam]) v = i % w.segs == a.eos / kSeg ? 0.f : -INFINITY;
         return Cand{total_key(beam, v), (uint32_t)i};
       });
-  for (int i = threadIdx.x; i < n_seg; i += kThreads) {
+  for (int i = threadIdx.x; i < n_seg; i += kPick) {
     const int beam = (int)L.idx[i] / w.segs;
     chosen[i] = make_int2(beam, ((int)L.idx[i] % w.segs) * kSeg);
   }
+  // the best of their elements: index beam * V + token (the maxima of n segments are n of them)
+  const uint32_t floor = n_seg == a.n ? (uint32_t)(L.key[a.n - 1] >> 32) : 0u;
   __syncthreads();
-  // the best of their elements: index beam * V + token
   const int n_out = block_select(
-      L, a.n, n_seg * kSeg,
+      L, a.n, n_seg * kSeg, floor,
       [&](int i) {
         const int2 g = chosen[i / kSeg];
         const int t = min(g.y + i % kSeg, a.V - 1), row = b * a.W + g.x;
         const float v = load_act<ACT>(a.logits, (size_t)row * a.ld + t) + 0.0f;
         return a.allowed && !(allowed_bits(a, row, t) & 1) ? -INFINITY : v;
       },
+      []() {},
       [&](int i, float v) {
         const int2 g = chosen[i / kSeg];
         const int t = g.y + i % kSeg;
         if (over[g.x]) v = t == a.eos ? 0.f : -INFINITY;
         return Cand{t < a.V ? total_key(g.x, v) : 0, (uint32_t)g.x * (uint32_t)a.V + (uint32_t)t};
       });
-  for (int i = threadIdx.x; i < a.n; i += kThreads) {
+  for (int i = threadIdx.x; i < a.n; i += kPick) {
     const size_t at = (size_t)b * a.n + i;
     const bool have = i < n_out;
     a.out_score[at] = have ? (float)key64_value(L.key[i]) : -INFINITY;
@@ -475,7 +528,7 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     k_beam_scan<ACT, U><<<(unsigned)blocks, kThreads, 0, s>>>(a, work);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_beam_pick<ACT, U><<<(unsigned)a.B, kThreads, 0, s>>>(a);
+    k_beam_pick<ACT, U><<<(unsigned)a.B, kPick, 0, s>>>(a);
     return hipGetLastError();
   };
   auto units = [&](auto act) {
