@@ -48,26 +48,27 @@ __host__ __device__ inline BeamWs beam_ws(void* ws, int rows, int V, int U) {
   return w;
 }
 
-// exp(v - top) to 2e-10 (relative) for v <= top, top finite; what lies more than 700
+// exp(v - top) to 6e-11 (relative) for v <= top, top finite; what lies more than 700
 // below counts e^-700, nothing next to the top's 1.  v - top = n ln 2 + y with |y| <=
-// ln 2 / 2 (and what n, rounded from an fp32 product, may be off: 2^-13), the series
-// of e^y to y^8 / 8!, n into the exponent.  n comes as the low bits of n + 1.5 2^23,
-// where the sum rounds to a whole number.
+// ln 2 / 2; e^y is the polynomial of degree 7 that meets it at the 8 Chebyshev nodes of
+// |y| <= 0.34665 (5.6e-11 off at most); n goes into the exponent.  n comes as the low
+// bits of n + 1.5 2^52, where the sum rounds to a whole number.  One conversion and 14
+// operations in 64 bits: conversions and 32-bit steps between cost more than they save
+// (20 operations, two more conversions: 33 us for 134 MB of fp32 logits against 27).
 __device__ __forceinline__ double exp_below(float v, float top) {
-  constexpr float kWhole = 12582912.f;
-  const float m = fmaf(fmaxf(v - top, -700.f), 1.44269504f, kWhole);
+  constexpr double kWhole = 6755399441055744.0;
   const double d = fmax((double)v - (double)top, -700.0);
-  const double y = fma(-(double)(m - kWhole), 0.69314718055994530942, d);
-  double p = 1.0 / 40320;
-  p = fma(p, y, 1.0 / 5040);
-  p = fma(p, y, 1.0 / 720);
-  p = fma(p, y, 1.0 / 120);
-  p = fma(p, y, 1.0 / 24);
-  p = fma(p, y, 1.0 / 6);
-  p = fma(p, y, 0.5);
-  p = fma(p, y, 1.0);
-  p = fma(p, y, 1.0);
-  return __hiloint2double(__double2hiint(p) + (__float_as_int(m) << 20), __double2loint(p));
+  const double m = fma(d, 1.4426950408889634074, kWhole);
+  const double y = fma(-(m - kWhole), 0.69314718055994530942, d);
+  double p = 0.00019907597155120258;
+  p = fma(p, y, 0.001394860471507592);
+  p = fma(p, y, 0.008333283498489944);
+  p = fma(p, y, 0.04166621792289689);
+  p = fma(p, y, 0.16666666786439385);
+  p = fma(p, y, 0.5000000107872163);
+  p = fma(p, y, 0.9999999999955067);
+  p = fma(p, y, 0.9999999999594902);
+  return __hiloint2double(__double2hiint(p) + (__double2loint(m) << 20), __double2loint(p));
 }
 
 __device__ __forceinline__ float wave_max_f(float v) {
@@ -119,7 +120,8 @@ __device__ __forceinline__ void load_seg(const BeamArgs& a, int row, int s, int 
     if (t + N <= a.V) {
       if constexpr (ACT == MOE_ACT_BF16) {
         typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-        const u32x4_any r = *reinterpret_cast<const u32x4_any*>(reinterpret_cast<const uint16_t*>(a.logits) + at);
+        const u32x4_any r = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4_any*>(reinterpret_cast<const uint16_t*>(a.logits) + at));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           v[2 * i] = __uint_as_float(r[i] << 16);
@@ -127,7 +129,8 @@ __device__ __forceinline__ void load_seg(const BeamArgs& a, int row, int s, int 
         }
       } else {
         typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-        const f32x4_any r = *reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(a.logits) + at);
+        const f32x4_any r = __builtin_nontemporal_load(
+            reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(a.logits) + at));
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[4 * h + i] = r[i];
       }
@@ -220,14 +223,14 @@ struct PickLds {
 
 // The held candidates ranked (16 lanes each, counting those before it); the n first
 // stay, in order.  Returns how many there are.
-__device__ int rank_held(PickLds& L, int n) {
+__device__ __forceinline__ int rank_held(PickLds& L, int n) {
   __syncthreads();
   const int m = (int)L.count;
   for (int i0 = 0; i0 < m; i0 += kPick / 16) {
     const int i = i0 + (int)(threadIdx.x >> 4);
     const Cand c{L.key[min(i, m - 1)], L.idx[min(i, m - 1)]};
     int r = 0;
-#pragma unroll 4
+#pragma unroll 2
     for (int j = threadIdx.x & 15; j < m; j += 16) r += before(Cand{L.key[j], L.idx[j]}, c);
     r += (int)dpp_u<kDppXor1>((uint32_t)r);
     r += (int)dpp_u<kDppXor2>((uint32_t)r);
@@ -275,127 +278,113 @@ __device__ int block_select(PickLds& L, int n, int total, uint32_t floor, Load&&
       if (i < total) h[k] = (uint32_t)(cand(i, v[k]).key >> 32);
     }
   };
-  uint32_t best = 0;
-  for (int i0 = 0; i0 < total; i0 += kBatch) {
-    read(i0);
-    if (i0 == 0) ready();
-    if (floor && total > kBatch) break;  // (read and looked at below)
-    heads(i0);
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) best = max(best, h[k]);
-  }
   if (threadIdx.x == 0) { L.count = 0; L.edge = floor; }
-  if (!floor) {
-    best = max(best, dpp_u<kDppXor1>(best));
-    best = max(best, dpp_u<kDppXor2>(best));
-    if ((threadIdx.x & 3) == 0) L.head[threadIdx.x >> 2] = best;
-    __syncthreads();
-    // heads that are better, that are at least as good: each of the four threads counts a quarter
-    int more = 0, least = 0;
-    const uint4* h4 = reinterpret_cast<const uint4*>(L.head) + (threadIdx.x & 3) * (kPick / 64);
-#pragma unroll 8
-    for (int j = 0; j < kPick / 64; ++j) {
-      const uint4 o = h4[j];
-      more += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
-      least += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
-    }
-    more += (int)dpp_u<kDppXor1>((uint32_t)more);
-    more += (int)dpp_u<kDppXor2>((uint32_t)more);
-    least += (int)dpp_u<kDppXor1>((uint32_t)least);
-    least += (int)dpp_u<kDppXor2>((uint32_t)least);
-    if (more < n && least >= n) L.edge = best;  // (the n-th: every thread that gets here has the same)
-  }
-  __syncthreads();
-  const uint32_t edge = max(L.edge, 1u);  // (key 0 is no candidate)
+  uint32_t best = 0;
   Cand last{0, 0xffffffffu};  // the n-th held so far
-  for (int i0 = 0; i0 < total; i0 += kBatch) {
-    if (total > kBatch) {
-      read(i0);
-      heads(i0);
-    }
-    auto passes = [&](int k, Cand* c) {
-      if (h[k] < edge) return false;
-      const int i = i0 + k * kPick + (int)threadIdx.x;
-      *c = cand(i, v[k]);
-      return before(*c, last);
-    };
-    uint32_t mine = 0;
+#pragma unroll 1
+  for (int pass = floor ? 1 : 0; pass < 2; ++pass) {
+    if (pass == 1) __syncthreads();
+    const uint32_t edge = pass == 1 ? max(L.edge, 1u) : 0u;  // (key 0 is no candidate)
+#pragma unroll 1
+    for (int i0 = 0; i0 < total; i0 += kBatch) {
+      if (pass == 0 || floor || total > kBatch) {
+        read(i0);
+        if (i0 == 0 && (pass == 0 || floor)) ready();
+        heads(i0);
+      }
+      if (pass == 0) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      Cand c;
-      mine += passes(k, &c);
-    }
-    const uint32_t held = L.count;
-    __syncthreads();
-    uint32_t at = mine ? atomicAdd(&L.count, mine) : 0u;
-    __syncthreads();
-    const bool fits = L.count <= (uint32_t)kCap;
-    __syncthreads();
-    if (fits) {
-      if (mine) {
+        for (int k = 0; k < kHeld; ++k) best = max(best, h[k]);
+        continue;
+      }
+      uint32_t todo = 0;  // the values that pass the edge: few
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
-          Cand c;
-          if (passes(k, &c)) {
+      for (int k = 0; k < kHeld; ++k) todo |= (h[k] >= edge ? 1u : 0u) << k;
+      auto take = [&](int k) {
+        float val = v[0];
+#pragma unroll
+        for (int j = 1; j < kHeld; ++j) val = k == j ? v[j] : val;
+        const Cand c = cand(i0 + k * kPick + (int)threadIdx.x, val);
+        if (before(c, last)) {
+          const uint32_t at = atomicAdd(&L.count, 1u);
+          if (at < (uint32_t)kCap) {
             L.key[at] = c.key;
-            L.idx[at++] = c.idx;
+            L.idx[at] = c.idx;
           }
         }
-      }
+      };
+      const uint32_t held = L.count;
       __syncthreads();
-    } else {
+#pragma unroll 1
+      for (uint32_t t = todo; t; t &= t - 1) take(__ffs((int)t) - 1);
+      __syncthreads();
+      if (L.count <= (uint32_t)kCap) continue;  // (the same for the whole block)
+      __syncthreads();
       if (threadIdx.x == 0) L.count = held;
       __syncthreads();
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < kHeld; ++k) {
         if (L.count > kCap - kPick) {  // (the same for the whole block)
           if (rank_held(L, n) == n) last = Cand{L.key[n - 1], L.idx[n - 1]};
         }
         __syncthreads();
-        Cand c;
-        if (passes(k, &c)) {
-          const uint32_t to = atomicAdd(&L.count, 1u);
-          L.key[to] = c.key;
-          L.idx[to] = c.idx;
-        }
+        if ((todo >> k) & 1) take(k);
         __syncthreads();
       }
-      if (rank_held(L, n) == n) last = Cand{L.key[n - 1], L.idx[n - 1]};
+    }
+    if (pass == 0) {
+      best = max(best, dpp_u<kDppXor1>(best));
+      best = max(best, dpp_u<kDppXor2>(best));
+      if ((threadIdx.x & 3) == 0) L.head[threadIdx.x >> 2] = best;
+      __syncthreads();
+      // heads that are better, that are at least as good: each of the four threads counts a quarter
+      int more = 0, least = 0;
+      const uint4* h4 = reinterpret_cast<const uint4*>(L.head) + (threadIdx.x & 3) * (kPick / 64);
+#pragma unroll 4
+      for (int j = 0; j < kPick / 64; ++j) {
+        const uint4 o = h4[j];
+        more += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
+        least += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
+      }
+      more += (int)dpp_u<kDppXor1>((uint32_t)more);
+      more += (int)dpp_u<kDppXor2>((uint32_t)more);
+      least += (int)dpp_u<kDppXor1>((uint32_t)least);
+      least += (int)dpp_u<kDppXor2>((uint32_t)least);
+      if (more < n && least >= n) L.edge = best;  // (the n-th: every thread that gets here has the same)
     }
   }
   return rank_held(L, n);
 }
 
 template <int ACT, int U>
-__global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a) {
+__global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
   __shared__ __attribute__((aligned(16))) PickLds L;
   __shared__ double lse[64], score[64];  // lse NaN: the beam has no candidates
   __shared__ uint8_t over[64];           // finished beams
   __shared__ int2 chosen[128];           // beam and first token of the best segments
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const BeamWs w = beam_ws(a.ws, a.B * a.W, a.V, U);
+  // inv = 2^40 / segs, rounded up: exact for i < 2^25 (i < W segs <= 2^21, segs <= 2^15)
+  auto beam_of = [&](int i) { return (int)(((uint64_t)(uint32_t)i * inv) >> 40); };
   const double none = __longlong_as_double(0x7ff8000000000000ll);
   auto beams = [&]() {
     for (int i = wave; i < a.W; i += kPick / 64) {
       const int row = b * a.W + i;
       const float sc = a.scores[row];
       const bool fin = a.finished && a.finished[row];
-      double l = 0.0;
-      if (!fin) {
-        float top = -INFINITY;  // of the lane's units so far, and their sum relative to it
-        double sum = 0.0;
-        for (int u = lane; u < w.units; u += 64) {
-          const float t = w.top[(size_t)row * w.units + u];
-          const double su = w.sum[(size_t)row * w.units + u];  // (0 for a unit of -inf, NaN for one with a NaN)
-          const float m = fmaxf(top, t);
-          sum = sum * exp_below(top, m) + su * exp_below(t, m);
-          top = m;
-        }
-        const float all = wave_max_f(top);
-        sum = wave_sum_d(sum * exp_below(top, all));
-        top = all;
-        l = top > -INFINITY && top < INFINITY ? (double)top + log(sum) : none;
+      float top = -INFINITY;  // of the lane's units so far, and their sum relative to it
+      double sum = 0.0;
+      for (int u = lane; u < w.units; u += 64) {  // (a finished beam's are not written; its l is set below)
+        const float t = w.top[(size_t)row * w.units + u];
+        const double su = w.sum[(size_t)row * w.units + u];  // (0 for a unit of -inf, NaN for one with a NaN)
+        const float m = fmaxf(top, t);
+        sum = sum * exp_below(top, m) + su * exp_below(t, m);
+        top = m;
       }
+      const float all = wave_max_f(top);
+      sum = wave_sum_d(sum * exp_below(top, all));
+      double l = all > -INFINITY && all < INFINITY ? (double)all + log(sum) : none;
+      if (fin) l = 0.0;
       if (!(sc > -INFINITY && sc < INFINITY)) l = none;
       if (lane == 0) {
         lse[i] = l;
@@ -415,13 +404,13 @@ __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a) {
       L, a.n, a.W * w.segs, 0u,
       [&](int i) { return w.seg[(size_t)b * a.W * w.segs + i]; }, beams,
       [&](int i, float v) {
-        const int beam = i / w.segs;
-        if (over[beam]) v = i % w.segs == a.eos / kSeg ? 0.f : -INFINITY;
+        const int beam = beam_of(i);
+        if (over[beam]) v = i - beam * w.segs == a.eos / kSeg ? 0.f : -INFINITY;
         return Cand{total_key(beam, v), (uint32_t)i};
       });
   for (int i = threadIdx.x; i < n_seg; i += kPick) {
-    const int beam = (int)L.idx[i] / w.segs;
-    chosen[i] = make_int2(beam, ((int)L.idx[i] % w.segs) * kSeg);
+    const int beam = beam_of((int)L.idx[i]);
+    chosen[i] = make_int2(beam, ((int)L.idx[i] - beam * w.segs) * kSeg);
   }
   // the best of their elements: index beam * V + token (the maxima of n segments are n of them)
   const uint32_t floor = n_seg == a.n ? (uint32_t)(L.key[a.n - 1] >> 32) : 0u;
@@ -528,7 +517,7 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     k_beam_scan<ACT, U><<<(unsigned)blocks, kThreads, 0, s>>>(a, work);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_beam_pick<ACT, U><<<(unsigned)a.B, kPick, 0, s>>>(a);
+    k_beam_pick<ACT, U><<<(unsigned)a.B, kPick, 0, s>>>(a, (((uint64_t)1 << 40) + segs - 1) / segs);
     return hipGetLastError();
   };
   auto units = [&](auto act) {
