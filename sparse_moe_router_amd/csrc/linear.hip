@@ -291,48 +291,60 @@ hipError_t run_few(const LinearArgs& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- five to sixteen tokens
-template <int QF, int ACT, int W>
+// TB = 8 or 16 tokens at most.  A fragment of a group has TB + 1 slots of 16 bytes:
+// the tokens', zero from token T on, and one that stays zero, which the rows of A past
+// TB read.
+template <int QF, int ACT, int W, int TB>
+struct SomeLds {
+  static constexpr int ts = (TB + 1) * 16;
+  static constexpr int x = W * Stage<QF, 1, kChunk>::kBytes;
+  static size_t total(int K) {
+    const size_t nc = (K / kGroup + kChunk - 1) / kChunk;
+    return x + kParts<ACT> * nc * kChunk * 4 * ts;
+  }
+};
+
+template <int QF, int ACT, int W, int TB>
 __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using St = Stage<QF, 1, kChunk>;
-  constexpr int P = kParts<ACT>;
+  using L = SomeLds<QF, ACT, W, TB>;
+  constexpr int P = kParts<ACT>, ts = L::ts;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, q = lane >> 4;
   const int G = a.K / kGroup, nc = (G + kChunk - 1) / kChunk;
   char* wl = lds + wave * St::kBytes;
-  char* xl = lds + W * St::kBytes;  // [part][group][fragment][T | 1], then 16 zero bytes
-  const int ts = (a.T | 1) * 16, xpart = nc * kChunk * 4 * ts;
+  char* xl = lds + L::x;  // [part][group][fragment][slot]
+  const int xpart = nc * kChunk * 4 * ts;
   const int first = blockIdx.x * W + wave, stride = gridDim.x * W;
-  for (int o = threadIdx.x; o < nc * kChunk * 2; o += 64 * W) {  // half a group of every token
-    const int h = o & 1, g = o >> 1;
-    constexpr int B = 4;
-    for (int t0 = 0; t0 < a.T; t0 += B) {
-      XHalf<ACT> xb[B];
+  const int halves = nc * kChunk * 2;  // half groups of a token
+  for (int o0 = threadIdx.x; o0 < a.T * halves; o0 += 4 * 64 * W) {
+    XHalf<ACT> xb[4];
 #pragma unroll
-      for (int b = 0; b < B; ++b) {
-        xb[b] = XHalf<ACT>{};
-        if (g < G && t0 + b < a.T) xb[b] = load_half<ACT>(a.x, (size_t)(t0 + b) * a.ldx + g * kGroup + 16 * h);
-      }
+    for (int b = 0; b < 4; ++b) {
+      const int o = o0 + b * 64 * W, t = o / halves, g = (o % halves) >> 1;
+      xb[b] = XHalf<ACT>{};
+      if (t < a.T && g < G) xb[b] = load_half<ACT>(a.x, (size_t)t * a.ldx + g * kGroup + 16 * (o & 1));
+    }
 #pragma unroll
-      for (int b = 0; b < B; ++b) {
-        if (t0 + b >= a.T) break;
-        Frag x[2][P];
-        half_frags<QF>(xb[b], x);
+    for (int b = 0; b < 4; ++b) {
+      const int o = o0 + b * 64 * W, t = o / halves, g = (o % halves) >> 1;
+      if (t >= a.T) break;
+      Frag x[2][P];
+      half_frags<QF>(xb[b], x);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int p = 0; p < P; ++p)
-            *reinterpret_cast<Frag*>(xl + p * xpart + (g * 4 + 2 * h + k) * ts + (t0 + b) * 16) = x[k][p];
-      }
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<Frag*>(xl + p * xpart + (g * 4 + 2 * (o & 1) + k) * ts + t * 16) = x[k][p];
     }
   }
-  if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(xl + P * xpart)[threadIdx.x] = 0;
+  for (int o = threadIdx.x; o < P * nc * kChunk * 4; o += 64 * W)
+    for (int t = a.T; t <= TB; ++t) *reinterpret_cast<Frag*>(xl + o * ts + t * 16) = Frag{{0, 0, 0, 0}};
   St w;
   if (first < units) w.load(a, (int64_t)first * 16 * G, true, lane);
   __syncthreads();
-  const bool tok = col < a.T;
-  const char* xr = tok ? xl + q * ts + col * 16 : xl + P * xpart;
-  const int xg = tok ? 4 * ts : 0, xp = tok ? xpart : 0;
+  const char* xr = xl + q * ts + min(col, TB) * 16;
   const Frag off = offset_frag<QF>();
   const Unpack<QF> unpack;
 
@@ -343,7 +355,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units)
       const bool end = c + 1 == nc;
       if (!end || unit + stride < units)
         w.load(a, (int64_t)(end ? unit + stride : unit) * 16 * G + (end ? 0 : c + 1) * kChunk, true, lane);
-      const char* xc = xr + c * kChunk * xg;
+      const char* xc = xr + c * (kChunk * 4 * ts);
 #pragma unroll
       for (int g4 = 0; g4 < kChunk; g4 += 4) {
         const uint2 sc = *reinterpret_cast<const uint2*>(St::scale(wl, col, g4));
@@ -354,7 +366,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units)
           f32x4_v c0 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int p = 0; p < P; ++p) {
-            x[p] = *reinterpret_cast<const Frag*>(xc + p * xp + (g4 + u) * xg);
+            x[p] = *reinterpret_cast<const Frag*>(xc + p * xpart + (g4 + u) * (4 * ts));
             c0 = mfma_frag(x[p], off, c0);
           }
           const Frag b = unpack(lds_frag_word<QF>(St::codes(wl, col, g4 + u), q));
@@ -381,52 +393,51 @@ __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units)
   }
 }
 
-template <int QF, int ACT, int W>
-size_t some_lds(const LinearArgs& a) {
-  const size_t nc = (a.K / kGroup + kChunk - 1) / kChunk;
-  return (size_t)W * Stage<QF, 1, kChunk>::kBytes + kParts<ACT> * nc * kChunk * 4 * (a.T | 1) * 16 + 16;
-}
-template <int QF, int ACT, int W>
+template <int QF, int ACT, int W, int TB>
+bool some_fits(const LinearArgs& a) { return SomeLds<QF, ACT, W, TB>::total(a.K) <= kLds; }
+template <int QF, int ACT, int W, int TB>
 hipError_t run_some(const LinearArgs& a, hipStream_t s) {
-  const size_t lds = some_lds<QF, ACT, W>(a);
+  const size_t lds = SomeLds<QF, ACT, W, TB>::total(a.K);
   const int units = (a.N + 15) / 16, all = (units + W - 1) / W;
   int per = (int)(kLds / lds);  // blocks a CU holds
   if (per > 16 / W) per = 16 / W;
-  k_linear_some<QF, ACT, W><<<all < per * kCus ? all : per * kCus, 64 * W, lds, s>>>(a, units);
+  k_linear_some<QF, ACT, W, TB><<<all < per * kCus ? all : per * kCus, 64 * W, lds, s>>>(a, units);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- token tiles
+constexpr int kRowWaves = 4, kTileChunk = 8;  // waves of a part, groups of a chunk
+
 template <int QF, int ACT, int R, int TT, int S>
 struct TileLds {
-  static constexpr int C = 8;
+  static constexpr int RW = kRowWaves, C = kTileChunk;
   static constexpr int kX = kParts<ACT> * C * TT * 1024;  // x of a chunk
-  static constexpr int need = S * kX + 4 * S * Stage<QF, R, C>::kBytes;
-  static constexpr int join = (S - 1) * 4 * R * TT * 1024;
+  static constexpr int need = S * kX + RW * S * Stage<QF, R, C, 0>::kBytes;
+  static constexpr int join = (S - 1) * RW * R * TT * 1024;
   static constexpr int total = need > join ? need : join;
   static_assert(total <= (int)kLds, "LDS");
 };
 
 template <int QF, int ACT, int R, int TT, int S, int OCC>
-__global__ __launch_bounds__(256 * S) __attribute__((amdgpu_waves_per_eu(OCC))) void k_linear_tile(LinearArgs a) {
+__global__ __launch_bounds__(64 * kRowWaves * S) __attribute__((amdgpu_waves_per_eu(OCC))) void k_linear_tile(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using L = TileLds<QF, ACT, R, TT, S>;
-  constexpr int C = L::C;
-  using St = Stage<QF, R, C>;
+  constexpr int RW = kRowWaves, C = kTileChunk;
+  using St = Stage<QF, R, C, 0>;  // (cached: other token tiles read the same rows)
   constexpr int P = kParts<ACT>, kXS = ACT == MOE_ACT_BF16 ? 2 : 4;
-  constexpr int XF = TT * C / 8;       // half groups a thread stages
-  constexpr int kTokStep = 128 / C;    // tokens a pass of a part's threads covers
+  constexpr int XF = TT * C / (2 * RW);    // half groups a thread stages
+  constexpr int kTokStep = 32 * RW / C;    // tokens a pass of a part's threads covers
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = wave >> 2, col = lane & 15, q = lane >> 4;
+  const int part = wave / RW, rw = wave % RW, col = lane & 15, q = lane >> 4;
   const int G = a.K / kGroup;
-  const int row0 = (blockIdx.x * 4 + (wave & 3)) * (16 * R), tok0 = blockIdx.y * (16 * TT);
+  const int row0 = (blockIdx.x * RW + rw) * (16 * R), tok0 = blockIdx.y * (16 * TT);
   const int chunks = (G + C - 1) / C, pc = (chunks + S - 1) / S, w0 = part * pc;  // chunks w0 .. w0 + pc - 1 are this part's
   char* xl = lds + part * L::kX;
   char* wl = lds + S * L::kX + wave * St::kBytes;
 
   St w;
-  auto load_w = [&](int c) { w.load(a, (int64_t)row0 * G + (int64_t)(w0 + c) * C, w0 + c < chunks, lane); };
-  const int pt = threadIdx.x & 255, xh = pt & 1, xg = (pt >> 1) % C, xt = (pt >> 1) / C;
+  auto load_w = [&](int c) { w.load(a, (int64_t)row0 * G + (int64_t)(w0 + c) * C, c < pc && w0 + c < chunks, lane); };
+  const int pt = threadIdx.x % (64 * RW), xh = pt & 1, xg = (pt >> 1) % C, xt = (pt >> 1) / C;
   uint32_t xo[XF];  // byte offsets, past the end for tokens that are not there
 #pragma unroll
   for (int i = 0; i < XF; ++i) {
@@ -436,15 +447,11 @@ __global__ __launch_bounds__(256 * S) __attribute__((amdgpu_waves_per_eu(OCC))) 
   const auto xrs = rsrc(reinterpret_cast<const char*>(a.x) + (int64_t)tok0 * a.ldx * kXS,
                         (uint32_t)(((int64_t)(min(a.T - tok0, 16 * TT) - 1) * a.ldx + a.K) * kXS));
   XHalf<ACT> xr[XF];
-  auto load_x = [&](int c) {
-    const bool in = (w0 + c) * C + xg < G;
-    const uint32_t go = (uint32_t)(w0 + c) * (C * kGroup * kXS);
+  auto load_x = [&](int c, int i) {
+    const bool in = c < pc && (w0 + c) * C + xg < G;
+    const uint32_t o = in ? xo[i] + (uint32_t)(w0 + c) * (C * kGroup * kXS) : 0x80000000u;
 #pragma unroll
-    for (int i = 0; i < XF; ++i) {
-      const uint32_t o = in ? xo[i] + go : 0x80000000u;
-#pragma unroll
-      for (int k = 0; k < (int)(sizeof(xr[i].v) / 16); ++k) xr[i].v[k] = __builtin_amdgcn_raw_buffer_load_b128(xrs, o + 16 * k, 0, 0);
-    }
+    for (int k = 0; k < (int)(sizeof(xr[i].v) / 16); ++k) xr[i].v[k] = __builtin_amdgcn_raw_buffer_load_b128(xrs, o + 16 * k, 0, 0);
   };
   // a fragment's 16 tokens are rotated by a key of its half and group: writes (lanes
   // of many groups, one token) and reads (lanes of many tokens, one group) both
@@ -471,19 +478,20 @@ __global__ __launch_bounds__(256 * S) __attribute__((amdgpu_waves_per_eu(OCC))) 
   const Frag off = offset_frag<QF>();
   const Unpack<QF> unpack;
 
-  load_x(0);
+#pragma unroll
+  for (int i = 0; i < XF; ++i) load_x(0, i);
   load_w(0);
   for (int c = 0; c < pc; ++c) {
     if (c) __syncthreads();
     put_x();
     w.put(wl, G - (w0 + c) * C, lane);
-    if (c + 1 < pc) {
-      load_x(c + 1);
-      load_w(c + 1);
-    }
     __syncthreads();
+    load_w(c + 1);
 #pragma unroll
     for (int g = 0; g < C; ++g) {
+      // the next chunk's loads between the products (chunks past the last load nothing)
+#pragma unroll
+      for (int i = (g * XF + C - 1) / C; i < ((g + 1) * XF + C - 1) / C; ++i) load_x(c + 1, i);
       Frag x[TT][P];
       f32x4_v c0[TT];
 #pragma unroll
@@ -524,7 +532,7 @@ __global__ __launch_bounds__(256 * S) __attribute__((amdgpu_waves_per_eu(OCC))) 
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt)
-          *reinterpret_cast<f32x4_v*>(j + ((((part - 1) * 4 + (wave & 3)) * R + r) * TT + tt) * 256 + lane * 4) = acc[r][tt];
+          *reinterpret_cast<f32x4_v*>(j + ((((part - 1) * RW + rw) * R + r) * TT + tt) * 256 + lane * 4) = acc[r][tt];
     }
     __syncthreads();
     if (part > 0) return;
@@ -534,7 +542,7 @@ __global__ __launch_bounds__(256 * S) __attribute__((amdgpu_waves_per_eu(OCC))) 
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt)
-          acc[r][tt] += *reinterpret_cast<const f32x4_v*>(j + (((p * 4 + wave) * R + r) * TT + tt) * 256 + lane * 4);
+          acc[r][tt] += *reinterpret_cast<const f32x4_v*>(j + (((p * RW + rw) * R + r) * TT + tt) * 256 + lane * 4);
   }
   auto write = [&](auto out) {
     constexpr int OUT = decltype(out)::value;
@@ -557,8 +565,8 @@ __global__ __launch_bounds__(256 * S) __attribute__((amdgpu_waves_per_eu(OCC))) 
 
 template <int QF, int ACT, int R, int TT, int S, int OCC>
 hipError_t run_tile(const LinearArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + 64 * R - 1) / (64 * R)), (unsigned)((a.T + 16 * TT - 1) / (16 * TT)));
-  k_linear_tile<QF, ACT, R, TT, S, OCC><<<grid, 256 * S, TileLds<QF, ACT, R, TT, S>::total, s>>>(a);
+  const dim3 grid((unsigned)((a.N + 16 * kRowWaves * R - 1) / (16 * kRowWaves * R)), (unsigned)((a.T + 16 * TT - 1) / (16 * TT)));
+  k_linear_tile<QF, ACT, R, TT, S, OCC><<<grid, 64 * kRowWaves * S, TileLds<QF, ACT, R, TT, S>::total, s>>>(a);
   return hipGetLastError();
 }
 
@@ -698,17 +706,26 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
         return hipSuccess;
       }
       if (a.T <= 16) {
-        if (a.N >= 8192 && some_lds<QF, ACT, 8>(a) <= kLds) return run_some<QF, ACT, 8>(a, s);
+        auto some = [&](auto tb) {
+          constexpr int TB = decltype(tb)::value;
+          if (some_fits<QF, ACT, 8, TB>(a)) return run_some<QF, ACT, 8, TB>(a, s);
+          if (some_fits<QF, ACT, 4, TB>(a)) return run_some<QF, ACT, 4, TB>(a, s);
+          return run_mid<QF, ACT>(a, s);
+        };
+        if (a.N >= 8192) return a.T <= 8 ? some(std::integral_constant<int, 8>{}) : some(std::integral_constant<int, 16>{});
         return run_mid<QF, ACT>(a, s);
       }
       if (64 * a.ldx * (ACT == MOE_ACT_BF16 ? 2 : 4) >= (int64_t)1 << 31) return run_mid<QF, ACT>(a, s);
+      // tiles of 64 rows x 64 tokens: enough for two blocks a CU with two row groups a wave; enough for
+      // one block a CU; too few, K split over four groups of waves (T = 64, 2048 x 2048: 30.7 -> 9.4 us)
       const int64_t r64 = (a.N + 63) / 64, t64 = (a.T + 63) / 64;
       if constexpr (ACT == MOE_ACT_BF16) {
-        if (r64 * t64 >= 1024) return run_tile<QF, ACT, 2, 4, 1, 2>(a, s);
-        if (r64 * t64 >= 192) return run_tile<QF, ACT, 1, 4, 2, 2>(a, s);
-        return run_tile<QF, ACT, 1, 2, 4, 4>(a, s);
+        if (r64 * t64 < 192) return run_tile<QF, ACT, 1, 2, 4, 4>(a, s);
+        if (a.T <= 32) return run_tile<QF, ACT, 1, 2, 2, 4>(a, s);
+        if (r64 * t64 < 1024) return run_tile<QF, ACT, 1, 4, 2, 2>(a, s);
+        return run_tile<QF, ACT, 2, 4, 1, 2>(a, s);
       } else {
-        return run_tile<QF, ACT, 1, 2, 2, 2>(a, s);
+        return run_tile<QF, ACT, 1, 2, 2, 2>(a, s);  // three parts of x fill the LDS
       }
     };
     if (a.act == MOE_ACT_BF16) return go(std::integral_constant<int, MOE_ACT_BF16>{});

@@ -200,20 +200,20 @@ __device__ __forceinline__ void load_frag(const void* x, size_t at, Frag (&o)[3]
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
-constexpr int kNt = 2;  // cache policy: each weight is read once, past the caches
+constexpr int kNt = 2;  // cache policy of weights that are read once: past the caches
 
-template <int QF>
+template <int QF, int NT = kNt>
 __device__ __forceinline__ typename CodeOf<QF>::T buf_codes(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-  if constexpr (QF == MOE_Q4_SYM_G32) return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kNt);
-  else if constexpr (QF == MOE_Q3_SYM_G32) return __builtin_amdgcn_raw_buffer_load_b96(r, at, 0, kNt);
-  else return __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, kNt);
+  if constexpr (QF == MOE_Q4_SYM_G32) return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, NT);
+  else if constexpr (QF == MOE_Q3_SYM_G32) return __builtin_amdgcn_raw_buffer_load_b96(r, at, 0, NT);
+  else return __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, NT);
 }
 
 // 16 R rows x C groups of packed weights on their way from memory to the wave's
 // own LDS.  A load takes 64 / C rows, C consecutive groups of each (whole cache
 // lines); read back, a lane finds any group of its row.  LDS rows are padded so
 // that 16 rows at the same group lie in different banks.
-template <int QF, int R, int C>
+template <int QF, int R, int C, int NT = kNt>
 struct Stage {
   using T = typename CodeOf<QF>::T;
   static constexpr int kB = CodeOf<QF>::kBytes;
@@ -239,7 +239,7 @@ struct Stage {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t g = mine + (uint32_t)((16 * r + (64 / C) * i) * G);
-        c[r][i] = buf_codes<QF>(rc, g * kB);
+        c[r][i] = buf_codes<QF, NT>(rc, g * kB);
         s[r][i] = __builtin_amdgcn_raw_buffer_load_b16(rs, g * 2, 0, 0);
         if constexpr (kPlanes == 2) m[r][i] = __builtin_amdgcn_raw_buffer_load_b16(rm, g * 2, 0, 0);
       }
