@@ -2,8 +2,9 @@
 // arithmetic: linear_frag.h).  Five kernels by the number of tokens T, all with
 // the weights' loads past the caches and whole cache lines per row:
 //
-// k_linear_one (T = 1).  A lane is a group: it unpacks 32 codes and multiplies
-// them with its 32 activations by v_dot2, 64 groups of a row a load.
+// k_linear_one (T = 1, and a few tokens of a small matrix, token by token).  A lane
+// is a group: it unpacks 32 codes and multiplies them with its 32 activations by
+// v_dot2, 64 groups of a row a load.
 //
 // k_linear_few (T = 2..4).  Matrix cores.  Products sum over the four lane rows,
 // which hold four DIFFERENT groups: so the A operand is block diagonal, row
@@ -47,6 +48,8 @@ __global__ __launch_bounds__(256) void k_linear_one(LinearArgs a) {
   const int G = a.K / kGroup;
   const int row0 = (blockIdx.x * 4 + wave) * (NR * RPI);
   if (row0 >= a.N) return;
+  const int t = blockIdx.y;
+  const size_t x0 = (size_t)t * a.ldx;
   const int64_t at = (int64_t)row0 * G, all = (int64_t)a.N * G;
   const uint32_t left = (uint32_t)min(all - at, (int64_t)1 << 26);
   const auto rc = rsrc(a.codes + at * kB, left * kB);
@@ -59,7 +62,7 @@ __global__ __launch_bounds__(256) void k_linear_one(LinearArgs a) {
     const int g = in ? g0 + gl : G - 1;
     XHalf<ACT> xr[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) xr[h] = load_half<ACT>(a.x, (size_t)g * kGroup + 16 * h);
+    for (int h = 0; h < 2; ++h) xr[h] = load_half<ACT>(a.x, x0 + (size_t)g * kGroup + 16 * h);
     typename CodeOf<QF>::T c[NR];
     uint16_t s[NR], m[NR];
 #pragma unroll
@@ -79,7 +82,9 @@ __global__ __launch_bounds__(256) void k_linear_one(LinearArgs a) {
     for (int r = 0; r < NR; ++r) {
       uint32_t words[4];
       frag_words<QF>(c[r], words);
-      float d = (QF == MOE_Q2_ASYM_G32 ? -1.f : -1.5f) * sx;
+      // bf16 x: the offset first; fp32 x: off every code, which is exact and keeps fp32's last bits
+      constexpr float kOff = QF == MOE_Q2_ASYM_G32 ? 1.f : 1.5f;
+      float d = ACT == MOE_ACT_BF16 ? -kOff * sx : 0.f;
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         const Frag b = unpack(words[f]);
@@ -90,8 +95,8 @@ __global__ __launch_bounds__(256) void k_linear_one(LinearArgs a) {
           } else {
             const u32x4& xa = QF == MOE_Q4_SYM_G32 ? xr[f >> 1].v[2 * (f & 1)] : xr[f >> 1].v[f & 1];
             const u32x4& xb = QF == MOE_Q4_SYM_G32 ? xr[f >> 1].v[2 * (f & 1) + 1] : xr[f >> 1].v[2 + (f & 1)];
-            d = fmaf(__uint_as_float(b.d[j] << 16), __uint_as_float(xa[j]), d);
-            d = fmaf(__uint_as_float(b.d[j] & 0xffff0000u), __uint_as_float(xb[j]), d);
+            d = fmaf(__uint_as_float(b.d[j] << 16) - kOff, __uint_as_float(xa[j]), d);
+            d = fmaf(__uint_as_float(b.d[j] & 0xffff0000u) - kOff, __uint_as_float(xb[j]), d);
           }
         }
       }
@@ -103,7 +108,7 @@ __global__ __launch_bounds__(256) void k_linear_one(LinearArgs a) {
   for (int r = 0; r < NR; ++r) {
     const int row = row0 + r * RPI + sub;
     const float v = seg_sum(acc[r], LR);
-    if (gl == 0 && row < a.N) store_y(a, 0, row, kOutFactor<QF> * v);
+    if (gl == 0 && row < a.N) store_y(a, t, row, kOutFactor<QF> * v);
   }
 }
 
@@ -112,12 +117,12 @@ hipError_t run_one(const LinearArgs& a, hipStream_t s) {
   constexpr int RPI = 64 / LR;
   auto go = [&](auto nr) {
     constexpr int NR = decltype(nr)::value, rows = 4 * NR * RPI;
-    k_linear_one<QF, ACT, LR, NR><<<(unsigned)((a.N + rows - 1) / rows), 256, 0, s>>>(a);
+    k_linear_one<QF, ACT, LR, NR><<<dim3((unsigned)((a.N + rows - 1) / rows), (unsigned)a.T), 256, 0, s>>>(a);
     return hipGetLastError();
   };
   // rows a wave: few while the chip is not full, many once it is
-  if (a.N <= 4096 * RPI) return go(std::integral_constant<int, 1>{});
-  if (a.N <= 65536 * RPI) return go(std::integral_constant<int, 4>{});
+  if ((int64_t)a.N * a.T <= 4096 * RPI) return go(std::integral_constant<int, 1>{});
+  if ((int64_t)a.N * a.T <= 65536 * RPI) return go(std::integral_constant<int, 4>{});
   return go(std::integral_constant<int, 8>{});
 }
 
@@ -692,18 +697,13 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
     };
     auto go = [&](auto act) {
       constexpr int ACT = decltype(act)::value;
-      if (a.T == 1) return one(act, a);
+      // small enough that one trip to memory is all there is: token by token, every wave its own rows
+      // (2048 x 2048: T = 4 4.8 -> 3.8 us, T = 8 5.4 -> 4.9; 4096 x 4096 at T = 4 8.0 against 6.9 the other way)
+      if (a.T == 1 || (a.T <= (ACT == MOE_ACT_BF16 ? 16 : 4) && (int64_t)a.N * a.K * a.T <= (int64_t)1 << 25))
+        return one(act, a);
       if (a.T <= 4) {
         if (few_fits<QF, ACT>(a)) return run_few<QF, ACT>(a, s);
-        for (int t = 0; t < a.T; ++t) {  // x too large for LDS: token by token
-          LinearArgs b = a;
-          b.T = 1;
-          b.x = reinterpret_cast<const char*>(a.x) + (size_t)t * a.ldx * (ACT == MOE_ACT_BF16 ? 2 : 4);
-          b.y = reinterpret_cast<char*>(a.y) + (size_t)t * a.ldy * (a.out == MOE_ACT_BF16 ? 2 : 4);
-          const hipError_t e = one(act, b);
-          if (e != hipSuccess) return e;
-        }
-        return hipSuccess;
+        return one(act, a);  // x too large for LDS
       }
       if (a.T <= 16) {
         auto some = [&](auto tb) {

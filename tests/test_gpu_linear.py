@@ -22,7 +22,8 @@ SIZES = [(1, 1, 32), (1, 17, 96), (1, 300, 2048), (2, 33, 64), (3, 100, 160), (4
          (300, 129, 2080)]
 # sizes that take the kernels of many rows: several rounds of a block, tiles of two row groups, x that does not fit LDS
 MANY = [(1, 70001, 96), (3, 40001, 64), (4, 33, 20000), (6, 8200, 96), (16, 9001, 544), (12, 8200, 1664), (130, 4200, 96),
-        (1030, 4100, 64), (20, 12300, 96), (16, 8193, 3712), (9, 8192, 1280)]
+        (1030, 4100, 64), (20, 12300, 96), (16, 8193, 3712), (9, 8192, 1280), (4, 4200, 2048), (3, 40001, 288),
+        (2, 9000, 2080), (16, 4100, 544), (6, 8200, 704)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -150,35 +151,37 @@ def test_random_values_many_rows(qfmt, act):
         assert (np.abs(y - want) <= lim + 2.0 ** -24 * (np.abs(want) + lim)).all(), (T, n, k)
 
 
-@pytest.mark.parametrize("T", (1, 4, 7, 40, 130))
-def test_strides_and_untouched_bytes(T):
+@pytest.mark.parametrize("T,n,k", ((1, 75, 160), (4, 75, 160), (7, 75, 160), (40, 75, 160), (130, 75, 160), (4, 8201, 1056),
+                                   (7, 8201, 608), (14, 8201, 608), (16, 4101, 544)))
+def test_strides_and_untouched_bytes(T, n, k):
     """x and y inside wider buffers (rows of x at odd multiples of 16 bytes, y at
     an odd element): same values, and nothing between the rows or behind them is
     written."""
     for act, out in (("bf16", "bf16"), ("f32", "f32")):
-        c = Case("q4_sym_g32", 75, 160, 3, False, act, out)
-        x = mo.round_act(np.random.default_rng(T).standard_normal((T, 160)), act)
+        c = Case("q4_sym_g32", n, k, 3, False, act, out)
+        x = mo.round_act(np.random.default_rng(T).standard_normal((T, k)), act)
         plain = call(c, c.x_dev(x), T, out)
-        wide = torch.full((T, 160 + 24), float("nan"), dtype=DT[act], device=gu.DEV)
-        wide[:, 8:168] = c.x_dev(x)
-        y = torch.full((T + 2, 75 + 6), 7.0, dtype=DT[out], device=gu.DEV)
-        api.moe_linear_q(c.lin, wide[:, 8:168], T, y[1:, 3:78])
+        wide = torch.full((T, k + 24), float("nan"), dtype=DT[act], device=gu.DEV)
+        wide[:, 8:8 + k] = c.x_dev(x)
+        y = torch.full((T + 2, n + 6), 7.0, dtype=DT[out], device=gu.DEV)
+        api.moe_linear_q(c.lin, wide[:, 8:8 + k], T, y[1:, 3:3 + n])
         torch.cuda.synchronize()
-        assert torch.equal(y[1:T + 1, 3:78], plain)
-        y[1:T + 1, 3:78] = 7.0
+        assert torch.equal(y[1:T + 1, 3:3 + n], plain)
+        y[1:T + 1, 3:3 + n] = 7.0
         assert torch.all(y == 7.0)
 
 
-@pytest.mark.parametrize("T", (2, 4, 16, 30, 100))
+@pytest.mark.parametrize("T,n,k", ((2, 130, 96), (4, 130, 96), (16, 130, 96), (30, 130, 96), (100, 130, 96), (4, 8200, 1056),
+                                   (8, 8200, 544), (16, 8200, 544), (16, 4100, 544)))
 @pytest.mark.parametrize("act", ("bf16", "f32"))
-def test_bad_rows_stay_alone(T, act):
+def test_bad_rows_stay_alone(T, n, k, act):
     """A NaN or an infinity in one token's x leaves the other tokens' rows with the bits they have without it."""
     for qfmt in FORMATS:
-        c = Case(qfmt, 130, 96, 11, False, act)
-        x = mo.round_act(np.random.default_rng(T).standard_normal((T, 96)), act)
+        c = Case(qfmt, n, k, 11, False, act)
+        x = mo.round_act(np.random.default_rng(T).standard_normal((T, k)), act)
         want = call(c, c.x_dev(x), T)
         bad = x.copy()
-        bad[0, 40], bad[T - 1, 95] = np.nan, np.inf
+        bad[0, 40], bad[T - 1, k - 1] = np.nan, np.inf
         got = call(c, c.x_dev(bad), T)
         assert torch.equal(got[1:T - 1], want[1:T - 1])
         assert not torch.isfinite(got[0]).any() and not torch.isfinite(got[T - 1]).any()
@@ -223,12 +226,13 @@ def test_large_rows_of_codes():
         del y
 
 
-def test_graph_replays_and_streams():
+@pytest.mark.parametrize("n,k", ((300, 512), (8300, 2080), (4300, 2112)))
+def test_graph_replays_and_streams(n, k):
     """Captured calls of every kernel, replayed with new inputs and the eager call in between; two streams at once."""
-    c = Case("q4_sym_g32", 300, 512, 21, False)
+    c = Case("q4_sym_g32", n, k, 21, False)
     r = np.random.default_rng(2)
-    bufs = {T: (bf16_dev(mo.round_act(r.standard_normal((T, 512)), "bf16")),
-                torch.zeros((T, 300), device=gu.DEV)) for T in (1, 4, 12, 60, 140)}
+    bufs = {T: (bf16_dev(mo.round_act(r.standard_normal((T, k)), "bf16")),
+                torch.zeros((T, n), device=gu.DEV)) for T in (1, 4, 8, 12, 60, 140)}
     for T, (x, y) in bufs.items():
         api.moe_linear_q(c.lin, x, T, y)
     torch.cuda.synchronize()
@@ -238,7 +242,7 @@ def test_graph_replays_and_streams():
             api.moe_linear_q(c.lin, x, T, y)
     for rep in range(4):
         for T, (x, y) in bufs.items():
-            x.copy_(bf16_dev(mo.round_act(r.standard_normal((T, 512)), "bf16")))
+            x.copy_(bf16_dev(mo.round_act(r.standard_normal((T, k)), "bf16")))
             y.fill_(float("nan"))
         g.replay()
         torch.cuda.synchronize()
@@ -246,7 +250,7 @@ def test_graph_replays_and_streams():
             assert torch.equal(call(c, x, T), y), (rep, T)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     want = {T: call(c, x, T) for T, (x, _) in bufs.items()}
-    outs = {T: [torch.zeros((T, 300), device=gu.DEV) for _ in range(6)] for T in bufs}
+    outs = {T: [torch.zeros((T, n), device=gu.DEV) for _ in range(6)] for T in bufs}
     torch.cuda.synchronize()
     for i in range(6):
         for T, (x, _) in bufs.items():
