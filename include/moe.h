@@ -283,7 +283,9 @@ typedef struct moe_beam {
  *                 one mask for every row).  Logits outside A_r count as -inf
  *                 whatever is stored there, NaN included.
  *   L_r         = log sum_{v in A_r} exp(logits[r][v])
- *   total(w, v) = scores[b][w] + (logits[r][v] - L_r)          (in 64 bits)
+ *   total(w, v) = scores[b][w] + (logits[r][v] - L_r)          (in 64 bits, the
+ *                 row's maximum taken off first: a row of one large value gives
+ *                 scores[b][w] - log |A_r|)
  * A beam with finished_opt[b][w] != 0 has the one candidate (w, eos) with
  * total scores[b][w], whatever its logits are.  A row whose score or L_r is not
  * finite (nothing allowed, a NaN or +inf among the allowed logits, a score of

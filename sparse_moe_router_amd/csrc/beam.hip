@@ -11,9 +11,9 @@
 // index: if n other segments come before a candidate's, each holds an element
 // that comes before the candidate).  The sum is held, and exp evaluated, in 64
 // bits: totals of different beams lie within 1e-7 of each other now and then, and
-// an L good to 1e-10 keeps them in order.
+// a logarithm good to 1e-10 keeps them in order.
 //
-// k_beam_pick, one block per sequence: L of every beam, the n best segments, then
+// k_beam_pick, one block per sequence: top and sum of every beam, the n best segments, then
 // the n best elements of those (read again, from the caches).
 #include "moe_device.h"
 #include "moe_internal.h"
@@ -54,7 +54,7 @@ __host__ __device__ inline BeamWs beam_ws(void* ws, int rows, int V, int U) {
 // |y| <= 0.34665 (5.6e-11 off at most); n goes into the exponent.  n comes as the low
 // bits of n + 1.5 2^52, where the sum rounds to a whole number.  One conversion and 14
 // operations in 64 bits: conversions and 32-bit steps between cost more than they save
-// (20 operations, two more conversions: 33 us for 134 MB of fp32 logits against 27).
+// (20 operations and two more conversions: 34 us for 134 MB of fp32 logits against 30).
 __device__ __forceinline__ double exp_below(float v, float top) {
   constexpr double kWhole = 6755399441055744.0;
   const double d = fmax((double)v - (double)top, -700.0);
@@ -359,7 +359,10 @@ __device__ int block_select(PickLds& L, int n, int total, uint32_t floor, Load&&
 template <int ACT, int U>
 __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
   __shared__ __attribute__((aligned(16))) PickLds L;
-  __shared__ double lse[64], score[64];  // lse NaN: the beam has no candidates
+  // a candidate's total is score + ((l - top) - ln sum exp(l - top)), in 64 bits: with top + ln sum rounded
+  // first, a row of one large value (a mask's lowest value in every place) would lose the logarithm
+  __shared__ double lse[64], score[64];  // the logarithm; NaN: the beam has no candidates
+  __shared__ float peak[64];             // top
   __shared__ uint8_t over[64];           // finished beams
   __shared__ int2 chosen[128];           // beam and first token of the best segments
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -383,11 +386,12 @@ __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
       }
       const float all = wave_max_f(top);
       sum = wave_sum_d(sum * exp_below(top, all));
-      double l = all > -INFINITY && all < INFINITY ? (double)all + log(sum) : none;
+      double l = all > -INFINITY && all < INFINITY ? log(sum) : none;
       if (fin) l = 0.0;
       if (!(sc > -INFINITY && sc < INFINITY)) l = none;
       if (lane == 0) {
         lse[i] = l;
+        peak[i] = fin ? 0.f : all;
         score[i] = (double)sc;
         over[i] = fin;
       }
@@ -397,7 +401,7 @@ __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
   auto total_key = [&](int beam, float v) -> uint64_t {
     const double l = lse[beam];
     if (l != l || v == -INFINITY) return 0;
-    return order_key64(score[beam] + ((double)v - l));
+    return order_key64(score[beam] + (((double)v - (double)peak[beam]) - l));
   };
   // the best segments: index beam * segs + segment; a finished beam has its token's segment only
   const int n_seg = block_select(
@@ -440,12 +444,14 @@ __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
 }
 
 // ---------------------------------------------------------------- reordering
-constexpr int kStates = 32;       // states per launch (the descriptors travel as kernel arguments)
+constexpr int kStates = 32;          // states per launch: the descriptors travel as kernel arguments,
+constexpr int kFewStates = 8;        // 2.2 KB of them, 0.6 KB where these are enough (a launch less than 1 us shorter)
 constexpr int kMaxBlocks = 1 << 16;  // of one state and sequence
 
+template <int NS>
 struct StateArgs {
-  moe_state s[kStates];
-  uint32_t end[kStates];  // blocks up to and with this state
+  moe_state s[NS];
+  uint32_t end[NS];  // blocks up to and with this state
   const int32_t* parent;
   int64_t ldp;
   int W, n;
@@ -455,8 +461,8 @@ struct StateArgs {
 // the column of all parents before it writes any, and nobody else touches that
 // column, so dst may be src, and a row that is its own parent is left alone there.
 // Block (x, sequence); x runs over the states' columns.
-template <int B, int WB>
-__global__ __launch_bounds__(kThreads) void k_reorder(StateArgs a) {
+template <int B, int WB, int NS>
+__global__ __launch_bounds__(kThreads) void k_reorder(StateArgs<NS> a) {
   typedef uint32_t Words __attribute__((ext_vector_type(B >= 8 ? B / 4 : 2)));
   using V = std::conditional_t<B >= 8, Words, std::conditional_t<B == 4, uint32_t, uint8_t>>;
   int k = 0;
@@ -538,20 +544,33 @@ hipError_t launch_beam_reorder(const moe_state* states, int n, const int32_t* pa
                    (uint64_t)st.dst_chunk_stride;
     return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
   };
-  auto run = [&](auto bytes, const StateArgs& a, int blocks, int nb) {
-    constexpr int BY = decltype(bytes)::value;
+  auto launch = [&](auto bytes, const auto& a, int blocks, int nb) {
+    constexpr int BY = decltype(bytes)::value, NS = (int)(sizeof(a.s) / sizeof(a.s[0]));
     const dim3 grid((unsigned)blocks, (unsigned)nb);
-    if (W <= 8) k_reorder<BY, 8><<<grid, kThreads, 0, s>>>(a);
-    else if (W <= 16) k_reorder<BY, 16><<<grid, kThreads, 0, s>>>(a);
-    else if (W <= 32) k_reorder<BY, 32><<<grid, kThreads, 0, s>>>(a);
-    else k_reorder<BY < 16 ? BY : 8, 64><<<grid, kThreads, 0, s>>>(a);
+    if (W <= 8) k_reorder<BY, 8, NS><<<grid, kThreads, 0, s>>>(a);
+    else if (W <= 16) k_reorder<BY, 16, NS><<<grid, kThreads, 0, s>>>(a);
+    else if (W <= 32) k_reorder<BY, 32, NS><<<grid, kThreads, 0, s>>>(a);
+    else k_reorder<BY < 16 ? BY : 8, 64, NS><<<grid, kThreads, 0, s>>>(a);
     return hipGetLastError();
+  };
+  auto run = [&](auto bytes, const StateArgs<kStates>& a, int blocks, int nb) {
+    if (a.n > kFewStates) return launch(bytes, a, blocks, nb);
+    StateArgs<kFewStates> f{};
+    for (int i = 0; i < a.n; ++i) {
+      f.s[i] = a.s[i];
+      f.end[i] = a.end[i];
+    }
+    f.parent = a.parent;
+    f.ldp = a.ldp;
+    f.W = a.W;
+    f.n = a.n;
+    return launch(bytes, f, blocks, nb);
   };
   for (int b0 = 0; b0 < B; b0 += 65535) {
     const int nb = B - b0 < 65535 ? B - b0 : 65535;
     for (int bytes = 16; bytes >= 1; bytes /= 4) {  // one launch for up to kStates states of a width
       const int col = bytes == 16 && W > 32 ? 8 : bytes;
-      StateArgs a{};
+      StateArgs<kStates> a{};
       a.parent = parent + b0 * ldp;
       a.ldp = ldp;
       a.W = W;

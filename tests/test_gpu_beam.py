@@ -43,9 +43,10 @@ def select_ref(logits, scores, n_out, finished=None, eos=-1, allowed=None):
             if v.size == 0 or np.isnan(v).any() or v.max() in (np.inf, -np.inf):
                 continue
             top = v.max()
-            lse = top + np.log(np.sum(np.exp(v - top)))
+            with np.errstate(under="ignore"):
+                total = np.log(np.sum(np.exp(v - top)))
             keep = v > -np.inf
-            totals.append(s + (v[keep] - lse))
+            totals.append(s + ((v[keep] - top) - total))
             flats.append(w * V + ids[keep])
         if not totals:
             continue
@@ -164,6 +165,21 @@ def test_select_rows_without_candidates():
         mask[0, 5] = mask[17, V - 1] = True
         check(lg, sc, 12, allowed=mask)
         check(lg, sc, 12, allowed=np.zeros((1, V), bool))
+
+
+@pytest.mark.parametrize("act", ("f32", "bf16"))
+@pytest.mark.parametrize("size", (1e4, 1e11, 1.5e38))
+def test_select_large_logits(size, act):
+    """Logits far apart: every exp but the largest's is zero or nearly so, the differences reach 3e38, and the sum of
+    a row of equal large logits is still ln V."""
+    r = np.random.default_rng(8)
+    lg = mo.round_act(np.clip(size * r.standard_normal((6, 5003)), -2 * size, 2 * size), act)
+    lg[5] = mo.round_act(np.full(1, size), act)[0]
+    sc = -np.sort(5 + 10 * r.random((2, 3)), axis=1)
+    check(lg, sc, 7, act=act)
+    got = check(lg[5:], sc[1:, 2:], 7, act=act)
+    assert np.array_equal(got[2][0], np.arange(7))
+    assert np.all(np.abs(got[0][0] - (float(np.float32(sc[1, 2])) - np.log(5003))) <= 2.0 ** -23 * 40)
 
 
 def test_select_long_rows_of_small_terms():
