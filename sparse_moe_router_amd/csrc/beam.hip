@@ -461,6 +461,11 @@ struct StateArgs {
 // the column of all parents before it writes any, and nobody else touches that
 // column, so dst may be src, and a row that is its own parent is left alone there.
 // Block (x, sequence); x runs over the states' columns.
+//   Bound by memory: 2 x the bytes moved (in place only what moves), a beam chosen
+// twice read once, by the same thread.  The stores are non-temporal: lines that leave
+// the caches early make room for the reads (610 MB into a second buffer 133 -> 125 us,
+// 4.9 TB/s, where a copy reaches 5.1; 3 GB in place 600 -> 572, 10 MB 8.6 -> 7.0);
+// non-temporal loads as well lose it again (144, 610, 8.2).
 template <int B, int WB, int NS>
 __global__ __launch_bounds__(kThreads) void k_reorder(StateArgs<NS> a) {
   typedef uint32_t Words __attribute__((ext_vector_type(B >= 8 ? B / 4 : 2)));
@@ -501,7 +506,7 @@ __global__ __launch_bounds__(kThreads) void k_reorder(StateArgs<NS> a) {
     for (int i = 0; i < WB; ++i) {
       if (i < a.W) {
         const int p = parent[i];
-        if ((uint32_t)p < (uint32_t)a.W && !(same && p == i)) *reinterpret_cast<V*>(to + i * s.dst_row_stride) = v[i];
+        if ((uint32_t)p < (uint32_t)a.W && !(same && p == i)) __builtin_nontemporal_store(v[i], reinterpret_cast<V*>(to + i * s.dst_row_stride));
       }
     }
   }
