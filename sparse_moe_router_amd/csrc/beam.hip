@@ -212,18 +212,21 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
 
 constexpr int kPick = 1024;  // threads of k_beam_pick
 constexpr int kCap = 2048;  // candidates held between two rankings
+struct Ranked {  // in order
+  uint64_t key[128];
+  uint32_t idx[128];
+};
 struct PickLds {
   uint64_t key[kCap];
   uint32_t idx[kCap];
-  uint64_t out_key[128];
-  uint32_t out_idx[128];
+  Ranked segments, out;
   uint32_t head[kPick / 4];
   uint32_t count, edge;
 };
 
-// The held candidates ranked (16 lanes each, counting those before it); the n first
-// stay, in order.  Returns how many there are.
-__device__ __forceinline__ int rank_held(PickLds& L, int n) {
+// The held candidates ranked (16 lanes each, counting those before it), the n first
+// into `to`.  Returns how many there are.
+__device__ __forceinline__ int rank_held(PickLds& L, Ranked& to, int n) {
   __syncthreads();
   const int m = (int)L.count;
   for (int i0 = 0; i0 < m; i0 += kPick / 16) {
@@ -236,29 +239,25 @@ __device__ __forceinline__ int rank_held(PickLds& L, int n) {
     r += (int)dpp_u<kDppXor2>((uint32_t)r);
     r += (int)dpp_u<kDppHalfMirror>((uint32_t)r);
     r += (int)dpp_u<kDppMirror>((uint32_t)r);
-    if (i < m && r < n && (threadIdx.x & 15) == 0) { L.out_key[r] = c.key; L.out_idx[r] = c.idx; }
+    if (i < m && r < n && (threadIdx.x & 15) == 0) { to.key[r] = c.key; to.idx[r] = c.idx; }
   }
   __syncthreads();
-  const int k = m < n ? m : n;
-  for (int i = threadIdx.x; i < k; i += kPick) { L.key[i] = L.out_key[i]; L.idx[i] = L.out_idx[i]; }
-  if (threadIdx.x == 0) L.count = k;
-  __syncthreads();
-  return k;
+  return m < n ? m : n;
 }
 
 constexpr int kHeld = 8;  // values a thread holds: 8192 candidates are read once
 
 // The n first of `total` candidates (load(i) the value from memory, cand(i, value)
-// the candidate; different indices), in order, in L.key / L.idx; returns how many
-// there are.  ready() runs once the first values are on their way.  floor: if not
-// 0, at least n candidates are known to have keys with upper halves >= floor.
-//   A first pass takes the best of every four threads and the n-th best of those: at
-// least n candidates are as good, so nothing worse is held in the second pass (by
-// the upper 32 bits of the key; usually little more than n candidates remain).  When
+// the candidate; different indices), in order, in `to`; returns how many there are.
+// ready() runs once the first values are on their way.  floor: if not 0, at least n
+// candidates are known to have keys with upper halves >= floor.
+//   A first pass takes the best of every four threads, and of those a value that n of
+// them reach: at least n candidates are as good, so nothing worse is held in the second
+// pass (by the upper 32 bits of the key; usually little more than n candidates remain).  When
 // the held ones do not fit, as with many equal totals, they are ranked 1024 at a
 // time and only what comes before the n-th of them is held from there on.
 template <typename Load, typename Ready, typename Make>
-__device__ int block_select(PickLds& L, int n, int total, uint32_t floor, Load&& load, Ready&& ready, Make&& cand) {
+__device__ int block_select(PickLds& L, Ranked& to, int n, int total, uint32_t floor, Load&& load, Ready&& ready, Make&& cand) {
   constexpr int kBatch = kPick * kHeld;
   float v[kHeld];
   uint32_t h[kHeld];
@@ -301,9 +300,10 @@ __device__ int block_select(PickLds& L, int n, int total, uint32_t floor, Load&&
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) todo |= (h[k] >= edge ? 1u : 0u) << k;
       auto take = [&](int k) {
-        float val = v[0];
-#pragma unroll
-        for (int j = 1; j < kHeld; ++j) val = k == j ? v[j] : val;
+        // v[k] by selects: with an index the compiler keeps v in LDS, at an address it works out from the
+        // launch's packet in host memory (3000 cycles)
+        const float a0 = k & 1 ? v[1] : v[0], a1 = k & 1 ? v[3] : v[2], a2 = k & 1 ? v[5] : v[4], a3 = k & 1 ? v[7] : v[6];
+        const float b0 = k & 2 ? a1 : a0, b1 = k & 2 ? a3 : a2, val = k & 4 ? b1 : b0;
         const Cand c = cand(i0 + k * kPick + (int)threadIdx.x, val);
         if (before(c, last)) {
           const uint32_t at = atomicAdd(&L.count, 1u);
@@ -325,7 +325,10 @@ __device__ int block_select(PickLds& L, int n, int total, uint32_t floor, Load&&
 #pragma unroll 1
       for (int k = 0; k < kHeld; ++k) {
         if (L.count > kCap - kPick) {  // (the same for the whole block)
-          if (rank_held(L, n) == n) last = Cand{L.key[n - 1], L.idx[n - 1]};
+          const int k = rank_held(L, to, n);
+          for (int i = threadIdx.x; i < k; i += kPick) { L.key[i] = to.key[i]; L.idx[i] = to.idx[i]; }
+          if (threadIdx.x == 0) L.count = k;
+          if (k == n) last = Cand{to.key[n - 1], to.idx[n - 1]};
         }
         __syncthreads();
         if ((todo >> k) & 1) take(k);
@@ -337,23 +340,35 @@ __device__ int block_select(PickLds& L, int n, int total, uint32_t floor, Load&&
       best = max(best, dpp_u<kDppXor2>(best));
       if ((threadIdx.x & 3) == 0) L.head[threadIdx.x >> 2] = best;
       __syncthreads();
-      // heads that are better, that are at least as good: each of the four threads counts a quarter
-      int more = 0, least = 0;
-      const uint4* h4 = reinterpret_cast<const uint4*>(L.head) + (threadIdx.x & 3) * (kPick / 64);
-#pragma unroll 4
-      for (int j = 0; j < kPick / 64; ++j) {
-        const uint4 o = h4[j];
-        more += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
-        least += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
+      // the n-th best head or a little less, bit by bit below what all heads share
+      if (threadIdx.x < 64) {
+        const uint4 o = reinterpret_cast<const uint4*>(L.head)[threadIdx.x];
+        const uint32_t hi = wave_max_u32(max(max(o.x, o.y), max(o.z, o.w)));
+        auto least = [](uint32_t h) { return h ? h : 0xffffffffu; };  // (0: nothing there)
+        const uint32_t lo = ~wave_max_u32(~min(min(least(o.x), least(o.y)), min(least(o.z), least(o.w))));
+        auto count = [&](uint32_t t) {
+          return __popcll(__ballot(o.x >= t)) + __popcll(__ballot(o.y >= t)) + __popcll(__ballot(o.z >= t)) +
+                 __popcll(__ballot(o.w >= t));
+        };
+        uint32_t at = 0;  // n heads are at or above it
+        if (hi == lo) {
+          at = count(lo) >= n ? lo : 0;
+        } else if (hi > lo && count(lo) >= n) {
+          int bit = 31 - __clz((int)(hi ^ lo));
+          at = (lo >> bit >> 1) << bit << 1;
+#pragma unroll 1
+          for (; bit >= 0; --bit) {
+            const uint32_t t = at | 1u << bit;
+            const int c = count(t);
+            if (c >= n) at = t;
+            if (c >= n && c <= n + 4) break;
+          }
+        }
+        if (threadIdx.x == 0) L.edge = at;
       }
-      more += (int)dpp_u<kDppXor1>((uint32_t)more);
-      more += (int)dpp_u<kDppXor2>((uint32_t)more);
-      least += (int)dpp_u<kDppXor1>((uint32_t)least);
-      least += (int)dpp_u<kDppXor2>((uint32_t)least);
-      if (more < n && least >= n) L.edge = best;  // (the n-th: every thread that gets here has the same)
     }
   }
-  return rank_held(L, n);
+  return rank_held(L, to, n);
 }
 
 template <int ACT, int U>
@@ -364,7 +379,6 @@ __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
   __shared__ double lse[64], score[64];  // the logarithm; NaN: the beam has no candidates
   __shared__ float peak[64];             // top
   __shared__ uint8_t over[64];           // finished beams
-  __shared__ int2 chosen[128];           // beam and first token of the best segments
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const BeamWs w = beam_ws(a.ws, a.B * a.W, a.V, U);
   // inv = 2^40 / segs, rounded up: exact for i < 2^25 (i < W segs <= 2^21, segs <= 2^15)
@@ -403,43 +417,41 @@ __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
     if (l != l || v == -INFINITY) return 0;
     return order_key64(score[beam] + (((double)v - (double)peak[beam]) - l));
   };
-  // the best segments: index beam * segs + segment; a finished beam has its token's segment only
+  // the best segments: index beam * 2^16 + segment; a finished beam has its token's segment only
   const int n_seg = block_select(
-      L, a.n, a.W * w.segs, 0u,
+      L, L.segments, a.n, a.W * w.segs, 0u,
       [&](int i) { return w.seg[(size_t)b * a.W * w.segs + i]; }, beams,
       [&](int i, float v) {
-        const int beam = beam_of(i);
-        if (over[beam]) v = i - beam * w.segs == a.eos / kSeg ? 0.f : -INFINITY;
-        return Cand{total_key(beam, v), (uint32_t)i};
+        const int beam = beam_of(i), seg = i - beam * w.segs;
+        if (over[beam]) v = seg == a.eos / kSeg ? 0.f : -INFINITY;
+        return Cand{total_key(beam, v), (uint32_t)(beam << 16 | seg)};
       });
-  for (int i = threadIdx.x; i < n_seg; i += kPick) {
-    const int beam = beam_of((int)L.idx[i]);
-    chosen[i] = make_int2(beam, ((int)L.idx[i] - beam * w.segs) * kSeg);
-  }
   // the best of their elements: index beam * V + token (the maxima of n segments are n of them)
-  const uint32_t floor = n_seg == a.n ? (uint32_t)(L.key[a.n - 1] >> 32) : 0u;
-  __syncthreads();
+  const uint32_t floor = n_seg == a.n ? (uint32_t)(L.segments.key[a.n - 1] >> 32) : 0u;
+  auto place = [&](int i) {  // (beam, token)
+    const uint32_t g = L.segments.idx[i / kSeg];
+    return make_int2((int)(g >> 16), (int)(g & 0xffffu) * kSeg + i % kSeg);
+  };
   const int n_out = block_select(
-      L, a.n, n_seg * kSeg, floor,
+      L, L.out, a.n, n_seg * kSeg, floor,
       [&](int i) {
-        const int2 g = chosen[i / kSeg];
-        const int t = min(g.y + i % kSeg, a.V - 1), row = b * a.W + g.x;
+        const int2 g = place(i);
+        const int t = min(g.y, a.V - 1), row = b * a.W + g.x;
         const float v = load_act<ACT>(a.logits, (size_t)row * a.ld + t) + 0.0f;
         return a.allowed && !(allowed_bits(a, row, t) & 1) ? -INFINITY : v;
       },
       []() {},
       [&](int i, float v) {
-        const int2 g = chosen[i / kSeg];
-        const int t = g.y + i % kSeg;
-        if (over[g.x]) v = t == a.eos ? 0.f : -INFINITY;
-        return Cand{t < a.V ? total_key(g.x, v) : 0, (uint32_t)g.x * (uint32_t)a.V + (uint32_t)t};
+        const int2 g = place(i);
+        if (over[g.x]) v = g.y == a.eos ? 0.f : -INFINITY;
+        return Cand{g.y < a.V ? total_key(g.x, v) : 0, (uint32_t)g.x * (uint32_t)a.V + (uint32_t)g.y};
       });
   for (int i = threadIdx.x; i < a.n; i += kPick) {
     const size_t at = (size_t)b * a.n + i;
     const bool have = i < n_out;
-    a.out_score[at] = have ? (float)key64_value(L.key[i]) : -INFINITY;
-    a.out_parent[at] = have ? (int)(L.idx[i] / (uint32_t)a.V) : -1;
-    a.out_token[at] = have ? (int)(L.idx[i] % (uint32_t)a.V) : -1;
+    a.out_score[at] = have ? (float)key64_value(L.out.key[i]) : -INFINITY;
+    a.out_parent[at] = have ? (int)(L.out.idx[i] / (uint32_t)a.V) : -1;
+    a.out_token[at] = have ? (int)(L.out.idx[i] % (uint32_t)a.V) : -1;
   }
 }
 
