@@ -294,7 +294,10 @@ typedef struct moe_beam {
  * the largest total, in descending order, equal totals by the lower w V + v;
  * out_score is the total rounded to fp32.  Where there are fewer candidates the rest are
  * (-1, -1, -inf).  Results do not depend on the launch or on other rows.
- * Workspace: at least moe_beam_workspace_bytes(beam), 256-byte aligned. */
+ * The outputs do not overlap the inputs, except that out_score may be scores
+ * itself when n_out == beams.
+ * Workspace: at least moe_beam_workspace_bytes(beam), 256-byte aligned; calls
+ * that may run at once have one each. */
 moe_status moe_beam_select(const moe_beam *beam, const void *logits, int64_t logits_stride, const float *scores,
                            const uint8_t *finished_opt, const uint32_t *allowed_opt, int64_t allowed_stride,
                            float *out_score, int32_t *out_parent, int32_t *out_token,

@@ -11,10 +11,15 @@
 // index: if n other segments come before a candidate's, each holds an element
 // that comes before the candidate).  The sum is held, and exp evaluated, in 64
 // bits: totals of different beams lie within 1e-7 of each other now and then, and
-// a logarithm good to 1e-10 keeps them in order.
+// a logarithm good to 1e-10 keeps them in order.  256 rows of 131072 fp32 logits (134
+// MB): 29.5 us, 4.5 TB/s, bound by memory and the 64-bit exp about equally.
 //
-// k_beam_pick, one block per sequence: top and sum of every beam, the n best segments, then
-// the n best elements of those (read again, from the caches).
+// k_beam_pick, one block per sequence: top and sum of every beam, the n best segments,
+// then the n best elements of those (read again, from the caches).  Latency bounds it:
+// 1 sequence x 4 beams x 32768 8.6 us, 32 x 8 x 131072 13 us.  In cycles, of 21 000 at
+// the former: start 1000, the beams' sums and logarithms 3200, an edge of the segments
+// 1000, held and ranked 4000, the elements' loads 2000, their totals 1900, held and
+// ranked 4000.  More blocks a sequence would need a third launch (2 us).
 #include "moe_device.h"
 #include "moe_internal.h"
 #include "topk.h"

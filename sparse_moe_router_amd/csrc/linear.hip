@@ -4,23 +4,35 @@
 //
 // k_linear_one (T = 1, and a few tokens of a small matrix, token by token).  A lane
 // is a group: it unpacks 32 codes and multiplies them with its 32 activations by
-// v_dot2, 64 groups of a row a load.
+// v_dot2, 64 groups of a row a load.  Memory bounds it where the matrix is large:
+// 131072 x 2048 4-bit 24.5 us, 6.2 TB/s (a plain read of as many bytes 6.4); 2048 x
+// 2048 2.9 us, a launch and one trip to memory.
 //
 // k_linear_few (T = 2..4).  Matrix cores.  Products sum over the four lane rows,
 // which hold four DIFFERENT groups: so the A operand is block diagonal, row
 // 4 q + t = token t in the lanes of group q and zero elsewhere.  The products of
 // the four fragments then add up to D[4 q + t] = the sum of group q for token t,
 // in the very lane that has the group's scale: one scale and 4 scale FMAs for 32
-// codes a lane.  x stays in LDS for the whole launch.
+// codes a lane.  x stays in LDS for the whole launch.  131072 x 2048 4-bit, T = 4: 30 us,
+// 5 TB/s (16 rows of A with a token in each, zeros behind them: 71 us, the scale FMAs).
 //
 // k_linear_some (T = 5..16).  The tokens fill the 16 rows of A and the four lane
-// rows hold one group: 4 scale FMAs for 8 codes a lane.  x stays in LDS.
+// rows hold one group: 4 scale FMAs for 8 codes a lane.  x stays in LDS.  Bound by the
+// vector instructions of a wave's chain (78 cycles a group and SIMD: unpack, scales, LDS)
+// and by the start, x and the first weights: 65536 x 2048 2-bit, T = 5 18.9 us (2.7
+// TB/s); 50021 x 2016 3-bit, T = 13 24.8 us (1.9 TB/s).
 //
 // k_linear_tile (more tokens).  Tiles of 16 R rows a wave and 16 TT tokens, x
-// staged chunk by chunk; S parts of the waves split K and join in LDS.
+// staged chunk by chunk; S parts of the waves split K and join in LDS.  Four scale FMAs
+// and three instructions of unpacking go with each MFMA, so the vector unit has more to
+// issue than the matrix cores: 1000 x 2048 x 8192 4-bit 61 us, 0.55 PFLOP/s, 63 % of it
+// in the products.  With one block a CU the loads, x's staging and the products follow
+// each other: 64 x 4096 x 16384 25 us (11, 7.5 and 16 us alone, partly overlapped).
+// Tiles of 32 x 128 a wave 62 against 64 us at T = 1000, of 64 x 64 the same: no gain.
 //
 // k_linear_mid: as k_linear_some with x read from the caches, the block's waves
-// splitting K: few rows, or x too large for LDS.
+// splitting K: few rows, or x too large for LDS.  2048 x 2048 4-bit, T = 16 5.7 us: the
+// waves' start, one trip to memory and the join.
 #include "linear_frag.h"
 
 namespace moe {

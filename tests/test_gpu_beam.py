@@ -395,6 +395,22 @@ def test_beam_search_steps():
             assert np.array_equal(fin.cpu().numpy().astype(bool), cfin)
 
 
+def test_scores_updated_in_place():
+    """out_score may be scores (n_out == beams), with more sequences than fit the chip at once."""
+    r = np.random.default_rng(12)
+    B, W, V = 600, 4, 700
+    lg, sc = gen(r, B, W, V, "f32")
+    want = run_select(lg, sc, W)
+    beam = api.Beam(batch=B, beams=W, vocab=V, n_out=W)
+    s = torch.from_numpy(sc.astype(np.float32)).to(gu.DEV)
+    outs = (torch.zeros((B, W), dtype=torch.int32, device=gu.DEV), torch.zeros((B, W), dtype=torch.int32, device=gu.DEV))
+    api.moe_beam_select(beam, torch.from_numpy(lg.astype(np.float32)).to(gu.DEV), s, s, *outs,
+                        ws=api.beam_workspace(beam, gu.DEV))
+    torch.cuda.synchronize()
+    for got, w in zip((s, *outs), want):
+        assert np.array_equal(got.cpu().numpy(), w)
+
+
 def test_captured_selections_do_not_share_a_workspace():
     """Two captured selections with a workspace each, replayed on two streams at once, keep their eager results."""
     r = np.random.default_rng(31)
