@@ -17,10 +17,12 @@
 // 5 TB/s (16 rows of A with a token in each, zeros behind them: 71 us, the scale FMAs).
 //
 // k_linear_some (T = 5..16).  The tokens fill the 16 rows of A and the four lane
-// rows hold one group: 4 scale FMAs for 8 codes a lane.  x stays in LDS.  Bound by the
-// vector instructions of a wave's chain (78 cycles a group and SIMD: unpack, scales, LDS)
-// and by the start, x and the first weights: 65536 x 2048 2-bit, T = 5 18.9 us (2.7
-// TB/s); 50021 x 2016 3-bit, T = 13 24.8 us (1.9 TB/s).
+// rows hold one group: 4 scale FMAs for 8 codes a lane.  Up to 8 tokens the rows are
+// the tokens twice, for two groups of two lane rows each, block diagonal as above: 4
+// scale FMAs for 16 codes (16384 x 4096, T = 8 13.3 -> 11.9 us).  x stays in LDS.  Bound
+// by the vector instructions of a wave's chain (unpack, scales, LDS) and by the start, x
+// and the first weights: 65536 x 2048 2-bit, T = 5 18.2 us (2.8 TB/s); 50021 x 2016
+// 3-bit, T = 13 24.4 us (1.9 TB/s).
 //
 // k_linear_tile (more tokens).  Tiles of 16 R rows a wave and 16 TT tokens, x
 // staged chunk by chunk; S parts of the waves split K and join in LDS.  Four scale FMAs
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units)
   char* wl = lds + wave * St::kBytes;
   char* xl = lds + L::x;  // [part][group][fragment][slot]
   const int xpart = nc * kChunk * 4 * ts;
-  const int first = blockIdx.x * W + wave, stride = gridDim.x * W;
+  const int first = blockIdx.x + wave * gridDim.x, stride = gridDim.x * W;  // (every CU the same number of waves)
   const int halves = nc * kChunk * 2;  // half groups of a token
   for (int o0 = threadIdx.x; o0 < a.T * halves; o0 += 4 * 64 * W) {
     XHalf<ACT> xb[4];
@@ -361,7 +363,12 @@ __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units)
   St w;
   if (first < units) w.load(a, (int64_t)first * 16 * G, true, lane);
   __syncthreads();
-  const char* xr = xl + q * ts + min(col, TB) * 16;
+  // kPair: lane rows 0, 1 hold one group, 2, 3 the next, two fragments each; else one group, a fragment each
+  constexpr bool kPair = TB == 8;
+  constexpr int kStep = kPair ? 2 : 1;  // groups (and fragments of a lane) a step
+  const int gq = kPair ? q >> 1 : 0, f0 = kPair ? 2 * (q & 1) : q;
+  const int slot = !kPair ? col : (col >> 3) == gq ? col & 7 : TB;
+  const char* xr = xl + (gq * 4 + f0) * ts + slot * 16;
   const Frag off = offset_frag<QF>();
   const Unpack<QF> unpack;
 
@@ -378,25 +385,32 @@ __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units)
         const uint2 sc = *reinterpret_cast<const uint2*>(St::scale(wl, col, g4));
         const uint2 mn = St::kPlanes == 2 ? *reinterpret_cast<const uint2*>(St::scale(wl, col, g4, 1)) : uint2{0, 0};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          Frag x[P];
+        for (int u = 0; u < 4; u += kStep) {
+          Frag x[P][kStep];
           f32x4_v c0 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            x[p] = *reinterpret_cast<const Frag*>(xc + p * xpart + (g4 + u) * (4 * ts));
-            c0 = mfma_frag(x[p], off, c0);
-          }
-          const Frag b = unpack(lds_frag_word<QF>(St::codes(wl, col, g4 + u), q));
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int f = 0; f < kStep; ++f) {
+              x[p][f] = *reinterpret_cast<const Frag*>(xc + p * xpart + ((g4 + u) * 4 + f) * ts);
+              c0 = mfma_frag(x[p][f], off, c0);
+            }
           f32x4_v d = c0;
 #pragma unroll
-          for (int p = 0; p < P; ++p) d = mfma_frag(x[p], b, d);
-          const uint32_t sw = u < 2 ? sc.x : sc.y;
-          const float s = f16_to_f32((uint16_t)(u & 1 ? sw >> 16 : sw));
+          for (int f = 0; f < kStep; ++f) {
+            const Frag b = unpack(lds_frag_word<QF>(St::codes(wl, col, g4 + u + gq), f0 + f));
+#pragma unroll
+            for (int p = 0; p < P; ++p) d = mfma_frag(x[p][f], b, d);
+          }
+          auto plane = [&](const uint2& v) {  // of the lane's group
+            const uint32_t w = u < 2 ? v.x : v.y;
+            return f16_to_f32((uint16_t)(kPair ? w >> (16 * gq) : u & 1 ? w >> 16 : w));
+          };
+          const float s = plane(sc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, d[i], acc[i]);
           if constexpr (St::kPlanes == 2) {
-            const uint32_t mw = u < 2 ? mn.x : mn.y;
-            const float m = -0.25f * f16_to_f32((uint16_t)(u & 1 ? mw >> 16 : mw));
+            const float m = -0.25f * plane(mn);
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = fmaf(m, c0[i], acc[i]);
           }
@@ -406,7 +420,15 @@ __global__ __launch_bounds__(64 * W) void k_linear_some(LinearArgs a, int units)
     const int row = unit * 16 + col;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (4 * q + i < a.T && row < a.N) store_y(a, 4 * q + i, row, kOutFactor<QF> * acc[i]);
+    {
+      float v = acc[i];
+      if constexpr (kPair) {  // the other groups' sum
+        uint32_t lo, hi;
+        swap32(__float_as_uint(v), &lo, &hi);
+        v = __uint_as_float(lo) + __uint_as_float(hi);
+      }
+      if (4 * q + i < a.T && row < a.N) store_y(a, 4 * q + i, row, kOutFactor<QF> * v);
+    }
   }
 }
 
@@ -415,10 +437,10 @@ bool some_fits(const LinearArgs& a) { return SomeLds<QF, ACT, W, TB>::total(a.K)
 template <int QF, int ACT, int W, int TB>
 hipError_t run_some(const LinearArgs& a, hipStream_t s) {
   const size_t lds = SomeLds<QF, ACT, W, TB>::total(a.K);
-  const int units = (a.N + 15) / 16, all = (units + W - 1) / W;
+  const int units = (a.N + 15) / 16;
   int per = (int)(kLds / lds);  // blocks a CU holds
   if (per > 16 / W) per = 16 / W;
-  k_linear_some<QF, ACT, W, TB><<<all < per * kCus ? all : per * kCus, 64 * W, lds, s>>>(a, units);
+  k_linear_some<QF, ACT, W, TB><<<units < per * kCus ? units : per * kCus, 64 * W, lds, s>>>(a, units);
   return hipGetLastError();
 }
 
@@ -720,6 +742,9 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
       if (a.T <= 16) {
         auto some = [&](auto tb) {
           constexpr int TB = decltype(tb)::value;
+          if constexpr (TB == 16 && ACT == MOE_ACT_BF16) {  // one large block a CU (T = 13 3-bit 27.0 -> 24.4 us)
+            if (some_fits<QF, ACT, 16, TB>(a)) return run_some<QF, ACT, 16, TB>(a, s);
+          }
           if (some_fits<QF, ACT, 8, TB>(a)) return run_some<QF, ACT, 8, TB>(a, s);
           if (some_fits<QF, ACT, 4, TB>(a)) return run_some<QF, ACT, 4, TB>(a, s);
           return run_mid<QF, ACT>(a, s);
