@@ -1,18 +1,19 @@
 // Beam search: the n best continuations of each sequence over beams and
 // vocabulary, and the move of the beams' states to follow their parents.
 //
-// Selection, two kernels.  A row's vocabulary is cut into segments of 512
+// Selection, two kernels.  A row's vocabulary is cut into segments of 256
 // consecutive tokens.
 //
-// k_beam_scan reads every logit once: a wave takes U segments of a row and writes
-// each segment's maximum and, over the U segments, (m, sum exp(l - m)).  No
+// k_beam_scan reads every logit once: a wave takes 2 U segments of a row and writes
+// each segment's maximum and, over all of them, (m, sum exp(l - m)).  No
 // selection happens here: the n best candidates of a sequence lie in the n
 // segments whose maxima are best (in the order of the totals, equal ones by
 // index: if n other segments come before a candidate's, each holds an element
 // that comes before the candidate).  The sum is held, and exp evaluated, in 64
 // bits: totals of different beams lie within 1e-7 of each other now and then, and
 // a logarithm good to 1e-10 keeps them in order.  256 rows of 131072 fp32 logits (134
-// MB): 29.5 us, 4.5 TB/s, bound by memory and the 64-bit exp about equally.
+// MB): 29.5 us, 4.5 TB/s, bound by memory and the 64-bit exp about equally.  Segments of 512
+// cost the pick more (24 beams, V 6035, 42 best 28 -> 22 us with 256).
 //
 // k_beam_pick, one block per sequence: top and sum of every beam, the n best segments,
 // then the n best elements of those (read again, from the caches).  Latency bounds it:
@@ -28,14 +29,15 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSeg = 512;  // tokens of a segment
+constexpr int kSeg = 256;    // tokens of a segment
+constexpr int kPiece = 512;  // tokens a wave reads at once: two segments
 
 // ---------------------------------------------------------------- scan
 struct BeamWs {
   double* sum;   // [rows][units]
   float* top;    // [rows][units]
   float* seg;    // [rows][segs] maxima
-  int units, segs;
+  int units, segs, pieces;
 };
 
 __host__ __device__ inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -43,7 +45,8 @@ __host__ __device__ inline size_t up256(size_t n) { return (n + 255) & ~(size_t)
 __host__ __device__ inline BeamWs beam_ws(void* ws, int rows, int V, int U) {
   BeamWs w;
   w.segs = (V + kSeg - 1) / kSeg;
-  w.units = (w.segs + U - 1) / U;
+  w.pieces = (V + kPiece - 1) / kPiece;
+  w.units = (w.pieces + U - 1) / U;
   char* p = reinterpret_cast<char*>(ws);
   w.sum = reinterpret_cast<double*>(p);
   p += up256((size_t)rows * w.units * 8);
@@ -76,17 +79,22 @@ __device__ __forceinline__ double exp_below(float v, float top) {
   return __hiloint2double(__double2hiint(p) + (__double2loint(m) << 20), __double2loint(p));
 }
 
-__device__ __forceinline__ float wave_max_f(float v) {
+// Maximum over the 32 lanes of a half wave, in each of them.
+__device__ __forceinline__ float half_max_f(float v) {
   v = fmaxf(v, dpp_f<kDppXor1>(v));
   v = fmaxf(v, dpp_f<kDppXor2>(v));
   v = fmaxf(v, dpp_f<kDppHalfMirror>(v));
   v = fmaxf(v, dpp_f<kDppMirror>(v));
   uint32_t a, b;
   swap16(__float_as_uint(v), &a, &b);
-  v = fmaxf(__uint_as_float(a), __uint_as_float(b));
+  return fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ float both_halves_max_f(float v) {
+  uint32_t a, b;
   swap32(__float_as_uint(v), &a, &b);
   return fmaxf(__uint_as_float(a), __uint_as_float(b));
 }
+__device__ __forceinline__ float wave_max_f(float v) { return both_halves_max_f(half_max_f(v)); }
 
 template <int CTRL>
 __device__ __forceinline__ double add_dpp(double v) {
@@ -112,15 +120,15 @@ __device__ __forceinline__ uint32_t allowed_bits(const BeamArgs& a, int row, int
   return a.allowed[(size_t)row * a.ld_allowed + (v >> 5)] >> (v & 31);
 }
 
-// 8 logits of one lane of segment s: tokens s 512 + 4 lane + {0..3} and the same + 256
+// 8 logits of one lane of piece s: tokens s 512 + 4 lane + {0..3} and the same + 256
 // (fp32) or s 512 + 8 lane + {0..7} (bf16); tokens that are not there or not
 // allowed are -inf.  (+ 0 makes a negative zero positive: the two are equal.)
 template <int ACT>
-__device__ __forceinline__ void load_seg(const BeamArgs& a, int row, int s, int lane, float (&v)[8]) {
+__device__ __forceinline__ void load_piece(const BeamArgs& a, int row, int s, int lane, float (&v)[8]) {
   constexpr int N = ACT == MOE_ACT_BF16 ? 8 : 4;
 #pragma unroll
   for (int h = 0; h < 8 / N; ++h) {
-    const int t = s * kSeg + 256 * h + N * lane;
+    const int t = s * kPiece + 256 * h + N * lane;
     const size_t at = (size_t)row * a.ld + t;
     if (t + N <= a.V) {
       if constexpr (ACT == MOE_ACT_BF16) {
@@ -165,24 +173,30 @@ __global__ __launch_bounds__(kThreads) void k_beam_scan(BeamArgs a, int64_t work
   for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[u][i] = -INFINITY;
-    if (unit * U + u < w.segs) load_seg<ACT>(a, row, unit * U + u, lane, v[u]);
+    if (unit * U + u < w.pieces) load_piece<ACT>(a, row, unit * U + u, lane, v[u]);
   }
   float mine = 0.f;
   bool bad = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float m = v[u][0];  // (fmaxf passes over a NaN)
-    bad |= v[u][0] != v[u][0];
+    // the maxima of the lane's first and last four (fmaxf passes over a NaN)
+    float m0 = fmaxf(fmaxf(v[u][0], v[u][1]), fmaxf(v[u][2], v[u][3]));
+    float m1 = fmaxf(fmaxf(v[u][4], v[u][5]), fmaxf(v[u][6], v[u][7]));
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      m = fmaxf(m, v[u][i]);
-      bad |= v[u][i] != v[u][i];
+    for (int i = 0; i < 8; ++i) bad |= v[u][i] != v[u][i];
+    // of the first segment in lanes 0..31, of the second in the others
+    float m = fmaxf(m0, m1);
+    if constexpr (ACT == MOE_ACT_F32) {
+      const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(m0), __float_as_uint(m1), false, false);
+      m = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
     }
-    m = wave_max_f(m);
-    if (lane == u) mine = m;
+    m = half_max_f(m);
+    if ((lane & 31) == u) mine = m;
     top = fmaxf(top, m);
   }
-  if (lane < U && unit * U + lane < w.segs) w.seg[(size_t)row * w.segs + unit * U + lane] = mine + 0.0f;
+  top = both_halves_max_f(top);
+  const int seg = 2 * (unit * U + (lane & 31)) + (lane >> 5);
+  if ((lane & 31) < U && seg < w.segs) w.seg[(size_t)row * w.segs + seg] = mine + 0.0f;
   double sum = 0.0;
   if (top > -INFINITY && top < INFINITY) {
 #pragma unroll
@@ -250,6 +264,9 @@ __device__ __forceinline__ int rank_held(PickLds& L, Ranked& to, int n) {
   return m < n ? m : n;
 }
 
+// Above this many candidates from a floor alone a first pass for a better edge costs less than ranking them (4 x 11
+// beams, V 520, 18 best: the 18th best of 33 segments lets 8000 through; 178 -> 14 us).
+constexpr int kFew = 384;
 constexpr int kHeld = 8;  // values a thread holds: 8192 candidates are read once
 
 // The n first of `total` candidates (load(i) the value from memory, cand(i, value)
@@ -287,6 +304,7 @@ __device__ int block_select(PickLds& L, Ranked& to, int n, int total, uint32_t f
   Cand last{0, 0xffffffffu};  // the n-th held so far
 #pragma unroll 1
   for (int pass = floor ? 1 : 0; pass < 2; ++pass) {
+    bool again = false;
     if (pass == 1) __syncthreads();
     const uint32_t edge = pass == 1 ? max(L.edge, 1u) : 0u;  // (key 0 is no candidate)
 #pragma unroll 1
@@ -323,6 +341,10 @@ __device__ int block_select(PickLds& L, Ranked& to, int n, int total, uint32_t f
 #pragma unroll 1
       for (uint32_t t = todo; t; t &= t - 1) take(__ffs((int)t) - 1);
       __syncthreads();
+      if (floor && L.count > (uint32_t)kFew) {  // the floor lets too many through: ranking them costs more than a first pass
+        again = true;
+        break;
+      }
       if (L.count <= (uint32_t)kCap) continue;  // (the same for the whole block)
       __syncthreads();
       if (threadIdx.x == 0) L.count = held;
@@ -339,6 +361,12 @@ __device__ int block_select(PickLds& L, Ranked& to, int n, int total, uint32_t f
         if ((todo >> k) & 1) take(k);
         __syncthreads();
       }
+    }
+    if (again) {
+      __syncthreads();
+      if (threadIdx.x == 0) { L.count = 0; L.edge = 0; }
+      floor = 0;
+      pass = -1;
     }
     if (pass == 0) {
       best = max(best, dpp_u<kDppXor1>(best));
@@ -386,7 +414,7 @@ __global__ __launch_bounds__(kPick) void k_beam_pick(BeamArgs a, uint64_t inv) {
   __shared__ uint8_t over[64];           // finished beams
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const BeamWs w = beam_ws(a.ws, a.B * a.W, a.V, U);
-  // inv = 2^40 / segs, rounded up: exact for i < 2^25 (i < W segs <= 2^21, segs <= 2^15)
+  // inv = 2^40 / segs, rounded up: exact for i < 2^24 (i < W segs <= 2^22, segs <= 2^16)
   auto beam_of = [&](int i) { return (int)(((uint64_t)(uint32_t)i * inv) >> 40); };
   const double none = __longlong_as_double(0x7ff8000000000000ll);
   auto beams = [&]() {
@@ -533,15 +561,15 @@ __global__ __launch_bounds__(kThreads) void k_reorder(StateArgs<NS> a) {
 
 size_t beam_ws_bytes(int B, int W, int V, int n, int act) {
   (void)n; (void)act;
-  const size_t rows = (size_t)B * W, segs = (V + kSeg - 1) / kSeg;  // one segment a unit at most
-  return up256(rows * segs * 8) + 2 * up256(rows * segs * 4);
+  const size_t rows = (size_t)B * W, segs = (V + kSeg - 1) / kSeg, pieces = (V + kPiece - 1) / kPiece;  // a piece a unit
+  return up256(rows * pieces * 8) + up256(rows * pieces * 4) + up256(rows * segs * 4);
 }
 
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
-  const int64_t rows = (int64_t)a.B * a.W, segs = (a.V + kSeg - 1) / kSeg;
+  const int64_t rows = (int64_t)a.B * a.W, segs = (a.V + kSeg - 1) / kSeg, pieces = (a.V + kPiece - 1) / kPiece;
   auto go = [&](auto act, auto u) {
     constexpr int ACT = decltype(act)::value, U = decltype(u)::value;
-    const int64_t work = rows * ((segs + U - 1) / U), blocks = (work + kThreads / 64 - 1) / (kThreads / 64);
+    const int64_t work = rows * ((pieces + U - 1) / U), blocks = (work + kThreads / 64 - 1) / (kThreads / 64);
     k_beam_scan<ACT, U><<<(unsigned)blocks, kThreads, 0, s>>>(a, work);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -549,8 +577,8 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     return hipGetLastError();
   };
   auto units = [&](auto act) {
-    // four segments a wave read 8 KiB at once; one while that leaves the chip idle
-    if (rows * segs >= 8192) return go(act, std::integral_constant<int, 4>{});
+    // four pieces a wave read 8 KiB at once; one while that leaves the chip idle
+    if (rows * pieces >= 8192) return go(act, std::integral_constant<int, 4>{});
     return go(act, std::integral_constant<int, 1>{});
   };
   if (a.act == MOE_ACT_BF16) return units(std::integral_constant<int, MOE_ACT_BF16>{});

@@ -107,7 +107,8 @@ def gen(r, B, W, V, act, spread=2.2):
 
 SELECT = [  # batch, beams, vocab, n_out
     (1, 1, 1, 1), (1, 1, 7, 3), (2, 3, 5, 20), (1, 4, 33, 8), (3, 2, 255, 4), (1, 5, 1000, 10), (2, 8, 4097, 16),
-    (1, 64, 301, 128), (4, 1, 50021, 1), (1, 3, 70001, 128), (5, 16, 2048, 32), (1, 2, 262144, 5), (70, 3, 600, 6)]
+    (1, 64, 301, 128), (4, 1, 50021, 1), (1, 3, 70001, 128), (5, 16, 2048, 32), (1, 2, 262144, 5), (70, 3, 600, 6), (4, 11, 520, 18),
+    (3, 24, 6035, 42), (2, 2, 256, 4), (2, 3, 257, 4), (1, 6, 769, 30)]
 
 
 @pytest.mark.parametrize("act", ("f32", "bf16"))
