@@ -29,8 +29,8 @@
 // and three instructions of unpacking go with each MFMA, so the vector unit has more to
 // issue than the matrix cores: 1000 x 2048 x 8192 4-bit 61 us, 0.55 PFLOP/s, 63 % of it
 // in the products.  With one block a CU the loads, x's staging and the products follow
-// each other: 64 x 4096 x 16384 25 us (11, 7.5 and 16 us alone, partly overlapped).
-// Tiles of 32 x 128 a wave 62 against 64 us at T = 1000, of 64 x 64 the same: no gain.
+// each other: 64 x 4096 x 16384 24 us.  Tiles of 32 x 128 a wave 62 against 64 us at T =
+// 1000, of 64 x 64 the same: no gain.
 //
 // k_linear_mid: as k_linear_some with x read from the caches, the block's waves
 // splitting K: few rows, or x too large for LDS.  2048 x 2048 4-bit, T = 16 5.7 us: the
@@ -753,16 +753,30 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
         return run_mid<QF, ACT>(a, s);
       }
       if (64 * a.ldx * (ACT == MOE_ACT_BF16 ? 2 : 4) >= (int64_t)1 << 31) return run_mid<QF, ACT>(a, s);
-      // tiles of 64 rows x 64 tokens: enough for two blocks a CU with two row groups a wave; enough for
-      // one block a CU; too few, K split over four groups of waves (T = 64, 2048 x 2048: 30.7 -> 9.4 us)
-      const int64_t r64 = (a.N + 63) / 64, t64 = (a.T + 63) / 64;
+      // By the number of tiles of 64 rows x 64 tokens.  More than one a CU: two row groups a wave, so that a block's
+      // x serves 128 rows (64 x 50021 x 2592: 85.8 -> 52.7 us, 24576 rows 44.4 -> 40.5), with 48 tokens a tile where
+      // that leaves fewer of them empty (T = 70, 44846 x 2592: 65.8 -> 56.1).  About one a CU: 128 rows x 32 tokens,
+      // K split over two groups of waves (64 x 16384 x 4096: 28.3 us, of 64 x 64 30.6, without the split 52).  Fewer:
+      // 16 tokens a tile, and K over four groups while those tiles leave the chip idle too (T = 64, 2048 x 2048: 6.5
+      // us, over two 7.4; T = 128, 4096 x 4096: 20.5 against 17.6).
+      const int64_t r64 = (a.N + 63) / 64, t64 = (a.T + 63) / 64, t48 = (a.T + 47) / 48;
       if constexpr (ACT == MOE_ACT_BF16) {
-        if (r64 * t64 < 192) return run_tile<QF, ACT, 1, 2, 4, 4>(a, s);
-        if (a.T <= 32) return run_tile<QF, ACT, 1, 2, 2, 4>(a, s);
-        if (r64 * t64 < 1024) return run_tile<QF, ACT, 1, 4, 2, 2>(a, s);
+        if (r64 * ((a.T + 15) / 16) <= 320) return run_tile<QF, ACT, 1, 1, 4, 4>(a, s);
+        if (r64 * t64 < 192) return run_tile<QF, ACT, 1, 1, 2, 4>(a, s);
+        if (a.T <= 32) {  // (many rows: T = 20, 100000 x 2592 76.7 -> 66.1 us, 24576 24.5 against 25.7)
+          return r64 <= 2 * kCus ? run_tile<QF, ACT, 1, 2, 2, 4>(a, s) : run_tile<QF, ACT, 1, 2, 1, 4>(a, s);
+        }
+        if (r64 * t64 <= kCus) return run_tile<QF, ACT, 2, 2, 2, 2>(a, s);
+        if (48 * t48 * 8 <= 64 * t64 * 7) return run_tile<QF, ACT, 2, 3, 1, 2>(a, s);
         return run_tile<QF, ACT, 2, 4, 1, 2>(a, s);
       } else {
-        return run_tile<QF, ACT, 1, 2, 2, 2>(a, s);  // three parts of x fill the LDS
+        // three parts of x a token: tiles of 128 x 32 (T = 500, 8192 x 2048: 78 us, of 64 x 32 with K split in two
+        // 135), of 128 x 16 with K split in two (T = 39, 10122 x 3296: 51 -> 28), few: of 64 x 16, in four (T = 17,
+        // 4974 x 7264: 60 -> 34)
+        const int64_t tiles = r64 * ((a.T + 31) / 32);
+        if (tiles < 192) return run_tile<QF, ACT, 1, 1, 4, 2>(a, s);
+        if (tiles < 512) return run_tile<QF, ACT, 2, 1, 2, 2>(a, s);
+        return run_tile<QF, ACT, 2, 2, 1, 2>(a, s);
       }
     };
     if (a.act == MOE_ACT_BF16) return go(std::integral_constant<int, MOE_ACT_BF16>{});

@@ -23,7 +23,8 @@ SIZES = [(1, 1, 32), (1, 17, 96), (1, 300, 2048), (2, 33, 64), (3, 100, 160), (4
 # sizes that take the kernels of many rows: several rounds of a block, tiles of two row groups, x that does not fit LDS
 MANY = [(1, 70001, 96), (3, 40001, 64), (4, 33, 20000), (6, 8200, 96), (16, 9001, 544), (12, 8200, 1664), (130, 4200, 96),
         (1030, 4100, 64), (20, 12300, 96), (16, 8193, 3712), (9, 8192, 1280), (4, 4200, 2048), (3, 40001, 288),
-        (2, 9000, 2080), (16, 4100, 544), (6, 8200, 704), (11, 8200, 2592), (7, 8193, 7200)]
+        (2, 9000, 2080), (16, 4100, 544), (6, 8200, 704), (11, 8200, 2592), (7, 8193, 7200), (20, 33000, 96),
+        (70, 12300, 160), (200, 5000, 96), (64, 17000, 96), (500, 1030, 288), (100, 40000, 64)]
 
 
 @pytest.fixture(scope="module", autouse=True)
