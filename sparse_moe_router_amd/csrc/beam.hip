@@ -513,14 +513,15 @@ struct StateArgs {
 // non-temporal loads as well lose it again (144, 610, 8.2).
 template <int B, int WB, int NS>
 __global__ __launch_bounds__(kThreads) void k_reorder(StateArgs<NS> a) {
-  typedef uint32_t Words __attribute__((ext_vector_type(B >= 8 ? B / 4 : 2)));
-  using V = std::conditional_t<B >= 8, Words, std::conditional_t<B == 4, uint32_t, uint8_t>>;
+  // (16 bytes at any address: the hardware takes them, and rows of an odd length start anywhere)
+  typedef uint32_t Words __attribute__((ext_vector_type(B >= 8 ? B / 4 : 2), aligned(1)));
+  using V = std::conditional_t<B >= 8, Words, std::conditional_t<B == 4, uint32_t, std::conditional_t<B == 2, uint16_t, uint8_t>>>;
   int k = 0;
   while (k + 1 < a.n && blockIdx.x >= a.end[k]) ++k;
   const moe_state& s = a.s[k];
   const uint32_t first = k ? a.end[k - 1] : 0u;
   const int b = blockIdx.y;
-  const bool same = s.src == s.dst;
+  const bool same = s.src == s.dst;  // (a rest keeps this: both move by the same bytes)
   const char* src = reinterpret_cast<const char*>(s.src) + (int64_t)b * a.W * s.src_row_stride;
   char* dst = reinterpret_cast<char*>(s.dst) + (int64_t)b * a.W * s.dst_row_stride;
   const int64_t piece = s.chunk_bytes / B, total = s.chunks * piece;
@@ -587,12 +588,14 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
 
 hipError_t launch_beam_reorder(const moe_state* states, int n, const int32_t* parent, int64_t ldp, int B, int W,
                                hipStream_t s) {
-  // the widest column that every address, stride and size of a state allows
+  // The widest column that every address, stride and size of a state allows.  A large state takes columns of 16
+  // bytes all the same, at any address, and one of those for the rest of its pieces: a launch more (39 states of 213
+  // rows of 66 bytes 66 -> 26 us).
   auto width = [&](const moe_state& st) {
     uint64_t all = reinterpret_cast<uintptr_t>(st.src) | reinterpret_cast<uintptr_t>(st.dst) | (uint64_t)st.chunk_bytes |
                    (uint64_t)st.src_row_stride | (uint64_t)st.dst_row_stride | (uint64_t)st.src_chunk_stride |
                    (uint64_t)st.dst_chunk_stride;
-    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
   };
   auto launch = [&](auto bytes, const auto& a, int blocks, int nb) {
     constexpr int BY = decltype(bytes)::value, NS = (int)(sizeof(a.s) / sizeof(a.s[0]));
@@ -618,7 +621,7 @@ hipError_t launch_beam_reorder(const moe_state* states, int n, const int32_t* pa
   };
   for (int b0 = 0; b0 < B; b0 += 65535) {
     const int nb = B - b0 < 65535 ? B - b0 : 65535;
-    for (int bytes = 16; bytes >= 1; bytes /= 4) {  // one launch for up to kStates states of a width
+    for (const int bytes : {16, 4, 2, 1}) {  // one launch for up to kStates states of a width
       const int col = bytes == 16 && W > 32 ? 8 : bytes;
       StateArgs<kStates> a{};
       a.parent = parent + b0 * ldp;
@@ -631,7 +634,17 @@ hipError_t launch_beam_reorder(const moe_state* states, int n, const int32_t* pa
           if (st.chunk_bytes == 0 || st.chunks == 0) continue;
           if (B * W == 1) st.src_row_stride = st.dst_row_stride = 0;
           if (st.chunks == 1) st.src_chunk_stride = st.dst_chunk_stride = 0;
-          if (width(st) != bytes) continue;
+          const int64_t wide = st.chunks * st.chunk_bytes < 8192 ? 0 : st.chunk_bytes / 16 * 16;
+          if (wide == 0) {
+            if (width(st) != bytes) continue;
+          } else if (bytes == 16) {
+            st.chunk_bytes = wide;
+          } else {
+            st.chunk_bytes -= wide;
+            st.src = reinterpret_cast<const char*>(st.src) + wide;
+            st.dst = reinterpret_cast<char*>(st.dst) + wide;
+          }
+          if (st.chunk_bytes == 0 || (wide && bytes < 16 && (width(st) < 4 ? width(st) : 4) != bytes)) continue;
           st.src = reinterpret_cast<const char*>(st.src) + (int64_t)b0 * W * st.src_row_stride;
           st.dst = reinterpret_cast<char*>(st.dst) + (int64_t)b0 * W * st.dst_row_stride;
           const int64_t want = (st.chunks * st.chunk_bytes / col + kThreads - 1) / kThreads;
@@ -642,6 +655,7 @@ hipError_t launch_beam_reorder(const moe_state* states, int n, const int32_t* pa
         if (a.n == kStates || (i == n && a.n > 0)) {
           const hipError_t e = bytes == 16  ? run(std::integral_constant<int, 16>{}, a, (int)blocks, nb)
                                : bytes == 4 ? run(std::integral_constant<int, 4>{}, a, (int)blocks, nb)
+                               : bytes == 2 ? run(std::integral_constant<int, 2>{}, a, (int)blocks, nb)
                                             : run(std::integral_constant<int, 1>{}, a, (int)blocks, nb);
           if (e != hipSuccess) return e;
           a.n = 0;

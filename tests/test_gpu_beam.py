@@ -296,6 +296,33 @@ def test_reorder_many_states_of_all_sizes():
     api.moe_beam_reorder([], parent, B, W)
 
 
+@pytest.mark.parametrize("W", (3, 40))
+def test_reorder_large_rows_at_odd_addresses(W):
+    """Rows above 8 KiB whose pieces are no multiple of 16 bytes and start anywhere: in place, and into another buffer
+    of another alignment; nothing beside the pieces is written."""
+    r = np.random.default_rng(W)
+    B = 2
+    parent = torch.from_numpy(r.integers(0, W, (B, W)).astype(np.int32)).to(gu.DEV)
+    for dtype, shape, part in ((torch.uint8, (4, 4099), (1, 4098)), (torch.uint8, (1, 9001), (3, 9000)),
+                               (torch.bfloat16, (213, 37), (2, 35)), (torch.float32, (5, 1003), (1, 1002)),
+                               (torch.uint8, (700, 31), (1, 16)), (torch.uint8, (700, 31), (0, 15))):
+        base = rand_state(r, (B * W, *shape), dtype)
+        s = base[:, :, part[0]:part[1]]
+        want = reorder_ref(s, s, parent, B, W)
+        dst = torch.full((B * W, shape[0], shape[1] + 2), 5, dtype=dtype, device=gu.DEV)
+        d = dst[:, :, 1:1 + part[1] - part[0]]
+        api.moe_beam_reorder([s], parent, B, W, dst=[d])
+        torch.cuda.synchronize()
+        assert torch.equal(d, want)
+        d.fill_(5)
+        assert torch.all(dst == 5)
+        other = base.clone()
+        other[:, :, part[0]:part[1]] = want
+        api.moe_beam_reorder([s], parent, B, W)
+        torch.cuda.synchronize()
+        assert torch.equal(base, other)
+
+
 def test_reorder_past_32_bit_offsets():
     """Rows of 1.5 GB: bytes past 2^32 of a state move."""
     rows, n = 4, 3 << 29
