@@ -17,7 +17,7 @@
 //
 // k_beam_pick, one block per sequence: top and sum of every beam, the n best segments,
 // then the n best elements of those (read again, from the caches).  Latency bounds it:
-// 1 sequence x 4 beams x 32768 8.6 us, 32 x 8 x 131072 13 us.  In cycles, of 21 000 at
+// 1 sequence x 4 beams x 32768 8.4 us, 32 x 8 x 131072 12.4 us.  In cycles, of 21 000 at
 // the former: start 1000, the beams' sums and logarithms 3200, an edge of the segments
 // 1000, held and ranked 4000, the elements' loads 2000, their totals 1900, held and
 // ranked 4000.  More blocks a sequence would need a third launch (2 us).

@@ -1,6 +1,6 @@
 // Dense projection with packed group-32 weights, y = x W^T + bias (fragments and
 // arithmetic: linear_frag.h).  Five kernels by the number of tokens T, all with
-// the weights' loads past the caches and whole cache lines per row:
+// whole cache lines of the weights per row and load, past the caches except for tiles:
 //
 // k_linear_one (T = 1, and a few tokens of a small matrix, token by token).  A lane
 // is a group: it unpacks 32 codes and multiplies them with its 32 activations by
@@ -21,8 +21,8 @@
 // the tokens twice, for two groups of two lane rows each, block diagonal as above: 4
 // scale FMAs for 16 codes (16384 x 4096, T = 8 13.3 -> 11.9 us).  x stays in LDS.  Bound
 // by the vector instructions of a wave's chain (unpack, scales, LDS) and by the start, x
-// and the first weights: 65536 x 2048 2-bit, T = 5 18.2 us (2.8 TB/s); 50021 x 2016
-// 3-bit, T = 13 24.4 us (1.9 TB/s).
+// and the first weights: 65536 x 2048 2-bit, T = 5 17.9 us (2.9 TB/s); 50021 x 2016
+// 3-bit, T = 13 24.3 us (1.9 TB/s).
 //
 // k_linear_tile (more tokens).  Tiles of 16 R rows a wave and 16 TT tokens, x
 // staged chunk by chunk; S parts of the waves split K and join in LDS.  Four scale FMAs
